@@ -255,6 +255,136 @@ jfa_status jfa_norm_quantize_mxfp8(const void* x, int64_t rows, int32_t D, const
                                    const float* beta, float eps, int layernorm, uint8_t* codes,
                                    uint8_t* scales, jfa_stream_t stream);
 
+/* MXFP4 (OCP MX v1.0: E2M1 elements, one E8M0 power-of-two scale per 32): the
+ * operands of jfa_matmul_mxfp4, for the projections on both sides of the
+ * attention ("Meta Enhances GEM Training Efficiency with Advanced LLM-Scale
+ * Innovations", "Implementing Ultra-Low-Precision Methods"; "GEM Training: How
+ * Meta Doubled the Efficiency of Its LLM-Scale Ads Foundation Model", opening
+ * summary: ultra-low precision in attention and MLP).
+ *
+ * An operand of R rows and K columns (the products contract over the columns)
+ * is two device buffers, 16-byte aligned:
+ *   codes  : uint8 [R][Kp / 2], Kp = K rounded up to a multiple of 32; column
+ *            2 i of a row is the low half of byte i, column 2 i + 1 the high
+ *            half; the codes behind column K are zero.  A code is sign (bit 3)
+ *            and index into 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   scales : E8M0 bytes in tiles of 128 rows x 4 blocks, 512 bytes each, in
+ *            the order the tensor core takes them: row r, block c (columns
+ *            32 c ..) at
+ *              ((r / 128) * T + c / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + c % 4
+ *            with T = ceil(K / 128); bytes of rows and blocks behind the
+ *            operand are zero.
+ * jfa_mxfp4_code_bytes / jfa_mxfp4_scale_bytes: the buffers' sizes (0 for a
+ * size outside [0, 2^30]). */
+size_t jfa_mxfp4_code_bytes(int64_t rows, int64_t cols);
+size_t jfa_mxfp4_scale_bytes(int64_t rows, int64_t cols);
+
+/* Quantises x [rows][cols] (device, dtype JFA_F32 or JFA_BF16, 16-byte
+ * aligned) to an MXFP4 operand.  Per block of 32 the shared exponent is
+ * X = floor(log2(amax)) - 2, clamped to [-127, 127] (-127 for an all-zero
+ * block); codes = RNE(x * 2^-X) saturated to +-6; scale byte = X + 127.  A
+ * block that holds an infinity or a NaN gets the scale byte 255 (NaN) and
+ * zero codes, so that every value of it, and every product with it, is NaN.
+ *   along_rows == 0: the operand is x (rows x cols), blocks run along a row
+ *   along_rows == 1: the operand is the transpose (cols x rows), blocks are
+ *                    32 consecutive rows of a column, zero-padded at the end:
+ *                    the form that a gradient's product needs
+ * Every byte of codes and scales is written.  rows, cols in [0, 2^30]; an
+ * empty x is a no-op.  JFA_ERR_INVALID_ARGUMENT for a bad size, dtype, NULL or
+ * misaligned pointer. */
+jfa_status jfa_quantize_mxfp4(const void* x, jfa_dtype dtype, int64_t rows, int64_t cols,
+                              int along_rows, uint8_t* codes, uint8_t* scales,
+                              jfa_stream_t stream);
+
+/* jfa_quantize_mxfp4 that also writes each element's value code * 2^X to
+ * dequant [rows][cols] (the layout and dtype of x; exact in both dtypes), for
+ * a straight-through step whose other passes run in bf16 or fp32. */
+jfa_status jfa_quantize_mxfp4_dequant(const void* x, jfa_dtype dtype, int64_t rows, int64_t cols,
+                                      int along_rows, uint8_t* codes, uint8_t* scales,
+                                      void* dequant, jfa_stream_t stream);
+
+/* Product of two MXFP4 operands on the tensor cores, fp32 accumulation, one
+ * rounding at the end:
+ *   out[i][j] = sum_k A[i][k] B[j][k]  (+ bias[j])  (+ out[i][j])
+ * A is an operand of m rows and k columns, B of n rows and k columns (a
+ * weight [n][k] as a linear layer keeps it); bias: device fp32 [n] or NULL;
+ * out: device [m][n], out_dtype JFA_F32 or JFA_BF16, 16-byte aligned, must not
+ * overlap the operands; accumulate != 0 adds to what out holds (gradient
+ * accumulation).  The gradients of a linear layer y = x w^T are products of
+ * the same kind: dx = dy w (operands dy along rows, w with along_rows = 1),
+ * dw = dy^T x (both with along_rows = 1).  The order of the sums depends only
+ * on the sizes: equal calls give equal bits.
+ * m, n, k in [0, 2^30]; m or n = 0 is a no-op, k = 0 an empty sum.
+ * workspace: jfa_mxfp4_workspace_bytes() bytes, 16-byte aligned, ZEROED by the
+ * caller once before its first use: it holds only the device error word,
+ * which stays set (JFA_ERR_TIMEOUT, results undefined) until jfa_check_error
+ * reads and clears it, so calls on several streams and captured graphs may
+ * share one.  Nothing is kept in it between calls. */
+size_t jfa_mxfp4_workspace_bytes(void);
+jfa_status jfa_matmul_mxfp4(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
+                            const uint8_t* a_scales, const uint8_t* b_codes,
+                            const uint8_t* b_scales, const float* bias, void* out,
+                            jfa_dtype out_dtype, int accumulate, void* workspace,
+                            size_t ws_bytes, jfa_stream_t stream);
+
+/* The norms before and after a block (an attention or MLP block of the model
+ * the attention runs in), fused with the block's gate and residual scale.
+ * For each row of `dim` elements of the residual stream x, the block's output
+ * b and the gate u:
+ *   p = post_norm(b)
+ *   y = x + s * act(u) * p       the residual stream behind the block
+ *   n = pre_norm(y)              the next block's input
+ *   norm(v) = (v - mu) / sqrt(mean((v - mu)^2) + eps) * gamma + beta, mu the
+ *   mean for JFA_NORM_LAYER and 0 for JFA_NORM_RMS; JFA_NORM_NONE: v itself
+ *   act: JFA_GATE_IDENTITY u, JFA_GATE_SILU u sigmoid(u), JFA_GATE_SIGMOID
+ *   sigmoid(u); JFA_GATE_NONE: no gate (1)
+ * in fp32, each result rounded once (n is taken from the unrounded y).  All
+ * tensors [rows][dim] in the descriptor's dtype (JFA_F32 or JFA_BF16), device,
+ * 16-byte aligned; s, gammas and betas device fp32 [dim], 16-byte aligned,
+ * NULL for 1 (s, gamma) and 0 (beta).  A gamma or beta that the descriptor's
+ * norm does not have, or a gate for JFA_GATE_NONE, is
+ * JFA_ERR_INVALID_ARGUMENT.  Results must not overlap the inputs. */
+typedef enum { JFA_NORM_NONE = 0, JFA_NORM_RMS = 1, JFA_NORM_LAYER = 2 } jfa_norm_kind;
+typedef enum {
+    JFA_GATE_NONE = 0,
+    JFA_GATE_IDENTITY = 1,
+    JFA_GATE_SILU = 2,
+    JFA_GATE_SIGMOID = 3
+} jfa_gate_kind;
+typedef struct {
+    int64_t rows;             /* >= 0 */
+    int32_t dim;              /* 1 .. 8192 (above: JFA_ERR_UNSUPPORTED) */
+    jfa_dtype dtype;
+    jfa_norm_kind post_norm;  /* of the block's output */
+    jfa_norm_kind pre_norm;   /* of the new residual stream */
+    jfa_gate_kind gate;
+    float eps;                /* > 0 */
+} jfa_block_norm;
+
+/* Forward: writes y and, with a pre_norm, n (ignored without one). */
+jfa_status jfa_block_norm_forward(const jfa_block_norm* desc, const void* x, const void* block,
+                                  const void* gate, const float* scale, const float* post_gamma,
+                                  const float* post_beta, const float* pre_gamma,
+                                  const float* pre_beta, void* y, void* n, jfa_stream_t stream);
+
+/* Backward: the gradients of <dy, y> + <dn, n> with respect to every input.
+ * Takes the forward's inputs (its values are recomputed), dy and, with a
+ * pre_norm, dn; writes dx, dblock and, with a gate, dgate (dtype), and each of
+ * the fp32 [dim] parameter gradients whose pointer is not NULL (overwritten;
+ * sums over the rows, zero for rows = 0), in a fixed order: equal calls give
+ * equal bits.  workspace: >= jfa_block_norm_workspace_bytes(desc) (0 for an
+ * invalid descriptor), 16-byte aligned, contents undefined before and after;
+ * one per call in flight. */
+size_t jfa_block_norm_workspace_bytes(const jfa_block_norm* desc);
+jfa_status jfa_block_norm_backward(const jfa_block_norm* desc, const void* x, const void* block,
+                                   const void* gate, const float* scale, const float* post_gamma,
+                                   const float* post_beta, const float* pre_gamma,
+                                   const float* pre_beta, const void* dy, const void* dn,
+                                   void* dx, void* dblock, void* dgate, float* dscale,
+                                   float* dpost_gamma, float* dpost_beta, float* dpre_gamma,
+                                   float* dpre_beta, void* workspace, size_t ws_bytes,
+                                   jfa_stream_t stream);
+
 /* The longest-first tile schedule that jfa_forward (backward = 0: items are
  * query tiles) or jfa_backward (backward = 1: items are key/value tiles) runs
  * over the jagged batch, so that short and long samples balance across SMs
@@ -336,7 +466,8 @@ const char* jfa_last_error(void);
 
 /* Kernel timing for measurement tools.  jfa_profile_enable(1) starts a fresh
  * record on the calling thread: from then on every kernel that jfa_forward,
- * jfa_backward, jfa_schedule or jfa_quantize_mxfp8 launches from this thread
+ * jfa_backward, jfa_schedule, a quantiser, jfa_matmul_mxfp4 or
+ * jfa_block_norm_* launches from this thread
  * is bracketed by two CUDA events recorded on the call's stream (the events
  * are created by the library and reused; no device memory is allocated).
  * jfa_profile_enable(0) stops recording and keeps the record.

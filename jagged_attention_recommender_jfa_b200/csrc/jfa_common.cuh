@@ -183,6 +183,13 @@ enum KernelId {
     K_NORM_QUANT,
     K_TC_BWD_SQ,
     K_TC_FWD_SQ,
+    K_MX4_ROWS,
+    K_MX4_COLS,
+    K_MX4_GEMM,
+    K_MX4_GEMM_PAIR,
+    K_BLOCK_NORM_FWD,
+    K_BLOCK_NORM_BWD,
+    K_BLOCK_NORM_SUM,
     K_COUNT
 };
 void prof_begin(cudaStream_t st);

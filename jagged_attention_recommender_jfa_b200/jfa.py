@@ -13,10 +13,11 @@ possible the import of the library fails loudly -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -42,7 +43,12 @@ EXPORTS = ("jfa_workspace_bytes", "jfa_forward", "jfa_backward", "jfa_quantize_m
            "jfa_profile_enable", "jfa_profile_read", "jfa_kernel_name",
            "jfa_forward_fixed_scratch", "jfa_partition", "jfa_backward_dbias",
            "jfa_block_offsets", "jfa_test_inject", "jfa_forward_mxfp8",
-           "jfa_norm_quantize_mxfp8")
+           "jfa_norm_quantize_mxfp8", "jfa_mxfp4_code_bytes", "jfa_mxfp4_scale_bytes",
+           "jfa_mxfp4_workspace_bytes", "jfa_quantize_mxfp4", "jfa_quantize_mxfp4_dequant",
+           "jfa_matmul_mxfp4", "jfa_block_norm_workspace_bytes", "jfa_block_norm_forward",
+           "jfa_block_norm_backward")
+NORM = {"none": 0, "rms": 1, "layer": 2}
+GATE = {"none": 0, "identity": 1, "silu": 2, "sigmoid": 3}
 JFA_TEST_FWD_SKIP_LOAD = 1
 PARTITION = {"lpt": 0, "bbs": 1}
 
@@ -60,6 +66,20 @@ class jfa_problem(ctypes.Structure):
                 ("total_kv", ctypes.c_int64), ("dtype", ctypes.c_int), ("scale", ctypes.c_float),
                 ("bias_kind", ctypes.c_int), ("relpos_len", ctypes.c_int32),
                 ("window", ctypes.c_int32)]
+
+
+class jfa_block_norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("post_norm", ctypes.c_int), ("pre_norm", ctypes.c_int), ("gate", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
+class MxOperand(NamedTuple):
+    """An MXFP4 operand of ``rows`` x ``cols`` (layouts in jfa.h)."""
+    codes: torch.Tensor    # uint8 [rows][ceil(cols / 32) * 16]
+    scales: torch.Tensor   # uint8, 128 x 4 tiles
+    rows: int
+    cols: int
 
 
 def lib_path() -> str:
@@ -110,6 +130,24 @@ def load():
         lib.jfa_forward_mxfp8.restype = i32
         lib.jfa_norm_quantize_mxfp8.argtypes = [P, i64, i32, P, P, ctypes.c_float, i32, P, P, P]
         lib.jfa_norm_quantize_mxfp8.restype = i32
+        for name in ("jfa_mxfp4_code_bytes", "jfa_mxfp4_scale_bytes"):
+            getattr(lib, name).argtypes = [i64, i64]
+            getattr(lib, name).restype = sz
+        lib.jfa_mxfp4_workspace_bytes.argtypes = []
+        lib.jfa_mxfp4_workspace_bytes.restype = sz
+        lib.jfa_quantize_mxfp4.argtypes = [P, i32, i64, i64, i32, P, P, P]
+        lib.jfa_quantize_mxfp4.restype = i32
+        lib.jfa_quantize_mxfp4_dequant.argtypes = [P, i32, i64, i64, i32, P, P, P, P]
+        lib.jfa_quantize_mxfp4_dequant.restype = i32
+        lib.jfa_matmul_mxfp4.argtypes = [i64, i64, i64, P, P, P, P, P, P, i32, i32, P, sz, P]
+        lib.jfa_matmul_mxfp4.restype = i32
+        PN = ctypes.POINTER(jfa_block_norm)
+        lib.jfa_block_norm_workspace_bytes.argtypes = [PN]
+        lib.jfa_block_norm_workspace_bytes.restype = sz
+        lib.jfa_block_norm_forward.argtypes = [PN] + [P] * 11
+        lib.jfa_block_norm_forward.restype = i32
+        lib.jfa_block_norm_backward.argtypes = [PN] + [P] * 19 + [sz, P]
+        lib.jfa_block_norm_backward.restype = i32
         lib.jfa_test_inject.argtypes = [i32]
         lib.jfa_test_inject.restype = i32
         lib.jfa_block_offsets.argtypes = [P, i32, i64, i32, P, P]
@@ -290,6 +328,74 @@ def jfa_norm_quantize_mxfp8(x, rows, D, gamma, beta, eps, layernorm, codes, scal
                                           _addr(scales), _stream(stream)))
 
 
+def jfa_mxfp4_code_bytes(rows, cols) -> int:
+    return int(load().jfa_mxfp4_code_bytes(int(rows), int(cols)))
+
+
+def jfa_mxfp4_scale_bytes(rows, cols) -> int:
+    return int(load().jfa_mxfp4_scale_bytes(int(rows), int(cols)))
+
+
+def jfa_mxfp4_workspace_bytes() -> int:
+    return int(load().jfa_mxfp4_workspace_bytes())
+
+
+def jfa_quantize_mxfp4(x, dtype, rows, cols, along_rows, codes, scales, stream=None):
+    _check(load().jfa_quantize_mxfp4(_addr(x), DTYPE.get(dtype, dtype), int(rows), int(cols),
+                                     int(bool(along_rows)), _addr(codes), _addr(scales),
+                                     _stream(stream)))
+
+
+def jfa_quantize_mxfp4_dequant(x, dtype, rows, cols, along_rows, codes, scales, dequant,
+                               stream=None):
+    _check(load().jfa_quantize_mxfp4_dequant(_addr(x), DTYPE.get(dtype, dtype), int(rows),
+                                             int(cols), int(bool(along_rows)), _addr(codes),
+                                             _addr(scales), _addr(dequant), _stream(stream)))
+
+
+def jfa_matmul_mxfp4(m, n, k, a_codes, a_scales, b_codes, b_scales, bias, out, out_dtype,
+                     accumulate, workspace, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(load().jfa_matmul_mxfp4(int(m), int(n), int(k), _addr(a_codes), _addr(a_scales),
+                                   _addr(b_codes), _addr(b_scales), _addr(bias), _addr(out),
+                                   DTYPE.get(out_dtype, out_dtype), int(bool(accumulate)),
+                                   _addr(workspace), int(ws_bytes), _stream(stream)))
+
+
+def make_block_norm(*, rows, dim, dtype="bf16", post_norm="rms", pre_norm="rms", gate="silu",
+                    eps=1e-5) -> jfa_block_norm:
+    return jfa_block_norm(int(rows), int(dim), DTYPE.get(dtype, dtype),
+                          NORM.get(post_norm, post_norm), NORM.get(pre_norm, pre_norm),
+                          GATE.get(gate, gate), float(eps))
+
+
+def jfa_block_norm_workspace_bytes(desc: jfa_block_norm) -> int:
+    return int(load().jfa_block_norm_workspace_bytes(ctypes.byref(desc)))
+
+
+def jfa_block_norm_forward(desc, x, block, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta,
+                           y, n, stream=None):
+    _check(load().jfa_block_norm_forward(ctypes.byref(desc), _addr(x), _addr(block), _addr(gate),
+                                         _addr(scale), _addr(post_gamma), _addr(post_beta),
+                                         _addr(pre_gamma), _addr(pre_beta), _addr(y), _addr(n),
+                                         _stream(stream)))
+
+
+def jfa_block_norm_backward(desc, x, block, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta,
+                            dy, dn, dx, dblock, dgate, dscale, dpost_gamma, dpost_beta, dpre_gamma,
+                            dpre_beta, workspace, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(load().jfa_block_norm_backward(ctypes.byref(desc), _addr(x), _addr(block), _addr(gate),
+                                          _addr(scale), _addr(post_gamma), _addr(post_beta),
+                                          _addr(pre_gamma), _addr(pre_beta), _addr(dy), _addr(dn),
+                                          _addr(dx), _addr(dblock), _addr(dgate), _addr(dscale),
+                                          _addr(dpost_gamma), _addr(dpost_beta), _addr(dpre_gamma),
+                                          _addr(dpre_beta), _addr(workspace), int(ws_bytes),
+                                          _stream(stream)))
+
+
 def jfa_test_inject(what: int):
     _check(load().jfa_test_inject(int(what)))
 
@@ -371,3 +477,188 @@ def attention_backward(problem, q, k, v, out, lse, dout, q_offsets, kv_offsets, 
     if check:
         jfa_check_error(ws, stream)
     return (dq, dk, dv, dbias) if want_dbias else (dq, dk, dv)
+
+
+# ---------------------------------------------------------------------------
+# Around the attention: MXFP4 operands and products, block norms.  These take
+# contiguous tensors, run on the tensors' own device and, unless ``stream``
+# says otherwise, on that device's current stream; with ``stream`` the results
+# are allocated on it too.
+# ---------------------------------------------------------------------------
+
+_TORCH_DTYPE = {torch.float32: JFA_F32, torch.bfloat16: JFA_BF16}
+
+
+def _need(ok: bool, msg: str):
+    if not ok:
+        raise JfaError(JFA_ERR_INVALID_ARGUMENT, msg)
+
+
+def _tensor(t, name, shape, dtypes, device):
+    """A contiguous CUDA tensor of the shape, one of the dtypes and on the device, or an error."""
+    _need(isinstance(t, torch.Tensor), f"{name}: a torch tensor is needed")
+    _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _need(t.dtype in dtypes, f"{name}: dtype {t.dtype} is not one of {dtypes}")
+    _need(t.is_cuda and (device is None or t.device == device), f"{name}: device {t.device}, expected {device or 'cuda'}")
+    _need(t.is_contiguous(), f"{name}: must be contiguous")
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The tensors' device, and the stream the call and its results belong to."""
+    with torch.cuda.device(device):
+        if stream is None or isinstance(stream, torch.cuda.Stream):
+            s = stream or torch.cuda.current_stream(device)
+        else:
+            s = torch.cuda.ExternalStream(int(stream), device=device)
+        _need(s.device == device, f"stream of {s.device} for tensors of {device}")
+        with torch.cuda.stream(s):
+            yield s
+
+
+def mxfp4_workspace(device) -> torch.Tensor:
+    """The zeroed workspace of :func:`matmul_mxfp4` (an error word; may be shared)."""
+    return torch.zeros(jfa_mxfp4_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def quantize_mxfp4(x, along_rows=False, want_dequant=False, stream=None):
+    """MXFP4 operand of ``x`` [rows, cols] (bf16 or fp32), or of its transpose
+    with ``along_rows`` (blocks of 32 rows).  With ``want_dequant`` also
+    returns the values it stands for, laid out like ``x``."""
+    _need(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a 2-D torch tensor is needed")
+    _tensor(x, "x", x.shape, tuple(_TORCH_DTYPE), None)
+    rows, cols = x.shape
+    r, c = (cols, rows) if along_rows else (rows, cols)
+    with _on(x.device, stream) as s:
+        u8 = dict(dtype=torch.uint8, device=x.device)
+        codes = torch.empty(r, (c + 31) // 32 * 16, **u8)
+        scales = torch.empty(jfa_mxfp4_scale_bytes(r, c), **u8)
+        if want_dequant:
+            dequant = torch.empty_like(x)
+            jfa_quantize_mxfp4_dequant(x, _TORCH_DTYPE[x.dtype], rows, cols, along_rows, codes,
+                                       scales, dequant, stream=s)
+            return MxOperand(codes, scales, r, c), dequant
+        jfa_quantize_mxfp4(x, _TORCH_DTYPE[x.dtype], rows, cols, along_rows, codes, scales, stream=s)
+        return MxOperand(codes, scales, r, c)
+
+
+def _operand(o, name, device=None):
+    _need(isinstance(o, MxOperand), f"{name}: an MxOperand is needed")
+    _need(o.rows >= 0 and o.cols >= 0, f"{name}: negative size")
+    _tensor(o.codes, f"{name}.codes", (o.rows, (o.cols + 31) // 32 * 16), (torch.uint8,), device)
+    _tensor(o.scales, f"{name}.scales", (jfa_mxfp4_scale_bytes(o.rows, o.cols),), (torch.uint8,),
+            o.codes.device)
+
+
+def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torch.bfloat16,
+                 accumulate=False, ws=None, stream=None, check=True):
+    """``a`` [m, k] times the transpose of ``b`` [n, k] (+ ``bias`` [n] fp32),
+    allocated in ``out_dtype`` unless ``out`` is given; ``accumulate`` adds to
+    ``out``.  ``ws``: :func:`mxfp4_workspace`; ``check`` as in
+    :func:`attention_forward`."""
+    _operand(a, "a")
+    dev = a.codes.device
+    _operand(b, "b", dev)
+    _need(a.cols == b.cols, f"a has {a.cols} columns, b {b.cols}")
+    m, n, k = a.rows, b.rows, a.cols
+    if bias is not None:
+        _tensor(bias, "bias", (n,), (torch.float32,), dev)
+    _need(out is not None or not accumulate, "accumulate needs out")
+    _need(out_dtype in _TORCH_DTYPE, f"out_dtype {out_dtype} is not one of {tuple(_TORCH_DTYPE)}")
+    if out is not None:
+        _tensor(out, "out", (m, n), tuple(_TORCH_DTYPE), dev)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(m, n, dtype=out_dtype, device=dev)
+        if ws is None:
+            ws = mxfp4_workspace(dev)
+        _need(ws.device == dev, f"ws: device {ws.device}, expected {dev}")
+        jfa_matmul_mxfp4(m, n, k, a.codes, a.scales, b.codes, b.scales, bias, out,
+                         _TORCH_DTYPE[out.dtype], accumulate, ws, stream=s)
+        if check:
+            jfa_check_error(ws, s)
+    return out
+
+
+def linear_mxfp4_forward(x, w: MxOperand, bias=None, ws=None, stream=None, check=True):
+    """``x`` [m, k] (quantised here) times the transpose of the weight operand
+    ``w`` [n, k] (``quantize_mxfp4`` of the weight), in the dtype of ``x``."""
+    a = quantize_mxfp4(x, stream=stream)
+    return matmul_mxfp4(a, w, bias=bias, out_dtype=x.dtype, ws=ws, stream=stream, check=check)
+
+
+def linear_mxfp4_backward(dy, x, w_t: MxOperand, dw=None, ws=None, stream=None, check=True):
+    """Gradients of :func:`linear_mxfp4_forward`: ``dx`` [m, k] in the dtype of
+    ``dy`` and ``dw`` [n, k] fp32 (added to ``dw`` where it is given), each a
+    product of operands quantised along its own contraction (the quantiser is
+    passed straight through).  ``w_t``: ``quantize_mxfp4(weight,
+    along_rows=True)``.  The bias's gradient is ``dy.sum(0)``."""
+    _need(isinstance(dy, torch.Tensor) and isinstance(x, torch.Tensor) and dy.dim() == 2
+          and x.dim() == 2 and dy.shape[0] == x.shape[0], "dy [m, n] and x [m, k] are needed")
+    _operand(w_t, "w_t")
+    _need(w_t.rows == x.shape[1] and w_t.cols == dy.shape[1],
+          f"w_t is {w_t.rows} x {w_t.cols}, expected {x.shape[1]} x {dy.shape[1]}")
+    if dw is not None:
+        _tensor(dw, "dw", (dy.shape[1], x.shape[1]), (torch.float32,), dy.device)
+    if ws is None:
+        with _on(dy.device, stream):
+            ws = mxfp4_workspace(dy.device)
+    kw = dict(ws=ws, stream=stream)
+    dx = matmul_mxfp4(quantize_mxfp4(dy, stream=stream), w_t, out_dtype=dy.dtype, check=False, **kw)
+    dw = matmul_mxfp4(quantize_mxfp4(dy, along_rows=True, stream=stream),
+                      quantize_mxfp4(x, along_rows=True, stream=stream), out=dw,
+                      out_dtype=torch.float32, accumulate=dw is not None, check=check, **kw)
+    return dx, dw
+
+
+def block_norm_workspace(desc: jfa_block_norm, device) -> torch.Tensor:
+    n = jfa_block_norm_workspace_bytes(desc)
+    if n == 0:
+        raise JfaError(JFA_ERR_INVALID_ARGUMENT, load().jfa_last_error().decode())
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _block_norm_args(desc, x, tensors, params):
+    _need(isinstance(x, torch.Tensor), "x: a torch tensor is needed")
+    dt = tuple(d for d, code in _TORCH_DTYPE.items() if code == desc.dtype)
+    for name, t in [("x", x)] + list(tensors.items()):
+        if t is not None:
+            _tensor(t, name, (desc.rows, desc.dim), dt, x.device)
+    for name, t in params.items():
+        if t is not None:
+            _tensor(t, name, (desc.dim,), (torch.float32,), x.device)
+
+
+def block_norm_forward(desc: jfa_block_norm, x, block, gate=None, scale=None, post_gamma=None,
+                       post_beta=None, pre_gamma=None, pre_beta=None, stream=None):
+    """Allocates and returns (y, n) of jfa_block_norm_forward; n is None
+    without a pre_norm."""
+    params = dict(scale=scale, post_gamma=post_gamma, post_beta=post_beta, pre_gamma=pre_gamma,
+                  pre_beta=pre_beta)
+    _block_norm_args(desc, x, dict(block=block, gate=gate), params)
+    with _on(x.device, stream) as s:
+        y = torch.empty_like(x)
+        n = torch.empty_like(x) if desc.pre_norm != NORM["none"] else None
+        jfa_block_norm_forward(desc, x, block, gate, *params.values(), y, n, stream=s)
+    return y, n
+
+
+def block_norm_backward(desc: jfa_block_norm, x, block, gate=None, scale=None, post_gamma=None,
+                        post_beta=None, pre_gamma=None, pre_beta=None, dy=None, dn=None, ws=None,
+                        stream=None):
+    """Allocates and returns the gradients of jfa_block_norm_backward as a dict
+    with the keys x, block, gate, scale, post_gamma, post_beta, pre_gamma and
+    pre_beta (None for an input that is None)."""
+    params = dict(scale=scale, post_gamma=post_gamma, post_beta=post_beta, pre_gamma=pre_gamma,
+                  pre_beta=pre_beta)
+    _block_norm_args(desc, x, dict(block=block, gate=gate, dy=dy, dn=dn), params)
+    with _on(x.device, stream) as s:
+        if ws is None:
+            ws = block_norm_workspace(desc, x.device)
+        _need(ws.device == x.device, f"ws: device {ws.device}, expected {x.device}")
+        g = {"x": torch.empty_like(x), "block": torch.empty_like(x),
+             "gate": None if gate is None else torch.empty_like(x)}
+        g.update({k: None if p is None else torch.empty_like(p) for k, p in params.items()})
+        jfa_block_norm_backward(desc, x, block, gate, *params.values(), dy, dn, *g.values(), ws,
+                                stream=s)
+    return g

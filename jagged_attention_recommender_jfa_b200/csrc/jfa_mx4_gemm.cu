@@ -14,11 +14,13 @@
 // needed.  Rows and columns behind the tensors' ends are read as zero and not
 // stored.
 //
-// The scale factors alternate between two TMEM slots; a slot is written again
-// once the MMAs of two steps ago, its last readers, have completed.
+// Each stage of the ring has its own TMEM columns for its scale factors.
 #include "jfa_mx4_gemm.cuh"
 
 namespace jfa {
+
+cudaError_t mx4_product_pair(Mx4Params& P, int64_t m, int64_t n, int64_t k, const uint8_t* ac, const uint8_t* as,
+                             const uint8_t* bc, const uint8_t* bs, int bn, int sms, cudaStream_t st);
 
 namespace {
 
@@ -37,10 +39,10 @@ struct Shape {
     static constexpr int kStages = BN == 64 ? 7 : 6;
     static constexpr uint32_t kPitch = BN + 4;            // floats per staged output row
     static constexpr uint32_t kSmem = kStages * kStage + 1024;
-    static constexpr uint32_t kTmem = BN == 64 ? 128 : 256;   // BN accumulator columns + 2 x 16 of scales
+    static constexpr uint32_t kTmem = 256;                // BN accumulator columns, 16 of scales per stage
     static_assert(kBM * kPitch * 4 <= kStages * kStage, "output staging reuses the ring");
     static_assert(kSmem <= 232448, "shared memory");
-    static_assert(BN + 32 <= (int)kTmem, "TMEM columns");
+    static_assert(BN + 16 * kStages <= (int)kTmem, "TMEM columns");
 };
 
 struct Bars {
@@ -49,42 +51,15 @@ struct Bars {
     int abort;
 };
 
-// Four consecutive columns of the result.
-__device__ __forceinline__ void store4_out(const Mx4Params& P, int64_t at, float4 v) {
-    if (P.out_bf16) {
-        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(P.out) + at;
-        if (P.accumulate) {
-            const float4 p = load4(o);
-            v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
-        }
-        store4(o, v);
-    } else {
-        float* o = reinterpret_cast<float*>(P.out) + at;
-        if (P.accumulate) {
-            const float4 p = load4(o);
-            v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
-        }
-        store4(o, v);
-    }
-}
-__device__ __forceinline__ void store1_out(const Mx4Params& P, int64_t at, float v) {
-    if (P.out_bf16) {
-        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(P.out) + at;
-        *o = __float2bfloat16_rn(P.accumulate ? v + __bfloat162float(*o) : v);
-    } else {
-        float* o = reinterpret_cast<float*>(P.out) + at;
-        *o = P.accumulate ? v + *o : v;
-    }
-}
-
 template <int BN>
-__global__ void __launch_bounds__(kThreads) mx4_gemm(const __grid_constant__ Mx4Params P, int n_tiles, int split) {
+__global__ void __launch_bounds__(kThreads) mx4_gemm(const __grid_constant__ Mx4Params P, int n_tiles, int split,
+                                                     uint32_t stage_bytes) {
     using S = Shape<BN>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;   // swizzle atoms are 1024-byte aligned
     uint8_t* const smem = smem_raw + (base - smem_u32(smem_raw));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = mx4::uniform_warp(), lane = threadIdx.x & 31;
     const int tile = blockIdx.x / split, rank = blockIdx.x - tile * split;
     const int m0 = (tile / n_tiles) * kBM, n0 = (tile % n_tiles) * BN;
     const int per = (P.k_stages + split - 1) / split;
@@ -111,58 +86,66 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm(const __grid_constant__ Mx4
     const uint32_t tmem = bars.tmem;
 
     if (warp == kTmaWarp) {
-        if (lane == 0) {
-            int issued = 0;
-            for (; issued < nk; ++issued) {
-                const int s = issued % S::kStages, ph = (issued / S::kStages) & 1;
-                if (issued >= S::kStages && !mbar_wait(&bars.empty[s], ph ^ 1, abort_flag, P.hdr)) break;
-                const uint32_t st = base + s * S::kStage, bar = smem_u32(&bars.full[s]);
-                const int kk = k0 + issued;
-                mbar_arrive_expect_tx(&bars.full[s], S::kStage);
-                mx4::tma_load_2d(st, &P.ta, bar, kk * 128, m0);
-                mx4::tma_load_2d(st + S::kA, &P.tb, bar, kk * 128, n0);
-                mx4::tma_load_2d(st + S::kA + S::kB, &P.tsa, bar, kk * 256, m0 >> 7);
-                mx4::tma_load_2d(st + S::kA + S::kB + S::kSf, &P.tsb, bar, kk * 256, n0 >> 7);
-            }
-            // copies in flight end before the CTA leaves, whatever happened
-            for (int i = max(0, issued - S::kStages); i < issued; ++i)
-                mbar_wait_drain(&bars.full[i % S::kStages], (i / S::kStages) & 1, P.hdr);
+        const uint32_t one = mx4::elect_one();
+        int issued = 0;
+        for (; issued < nk; ++issued) {
+            const int s = issued % S::kStages, ph = (issued / S::kStages) & 1;
+            if (issued >= S::kStages && !mx4::warp_wait(&bars.empty[s], ph ^ 1, abort_flag, P.hdr)) break;
+            const uint32_t st = base + s * S::kStage, bar = smem_u32(&bars.full[s]);
+            const int kk = k0 + issued;
+            mx4::expect_tx_one(one, &bars.full[s], stage_bytes);
+            mx4::tma_load_2d(one, st, &P.ta, bar, kk * 128, m0);
+            mx4::tma_load_2d(one, st + S::kA, &P.tb, bar, kk * 128, n0);
+            mx4::tma_load_2d(one, st + S::kA + S::kB, &P.tsa, bar, kk * 256, m0 >> 7);
+            mx4::tma_load_2d(one, st + S::kA + S::kB + S::kSf, &P.tsb, bar, kk * 256, n0 >> 7);
         }
+        // copies in flight end before the CTA leaves, whatever happened
+        for (int i = max(0, issued - S::kStages); i < issued; ++i)
+            mbar_wait_drain(&bars.full[i % S::kStages], (i / S::kStages) & 1, P.hdr);
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            // the second 64 rows of a scale tile are its columns 2 and 3
-            const uint32_t sfb_half = BN == 64 ? (uint32_t)((n0 >> 6) & 1) * 2u : 0u;
-            int done = 0;
-            for (; done < nk; ++done) {
-                const int s = done % S::kStages, ph = (done / S::kStages) & 1;
-                if (!mbar_wait(&bars.full[s], ph, abort_flag, P.hdr)) break;
-                if (done >= 2) {
-                    const int o = done - 2;
-                    if (!mbar_wait(&bars.empty[o % S::kStages], (o / S::kStages) & 1, abort_flag, P.hdr)) break;
+        const uint32_t one = mx4::elect_one();
+        // the second 64 rows of a scale tile are its columns 2 and 3
+        const uint32_t sfb_half = BN == 64 ? (uint32_t)((n0 >> 6) & 1) * 2u : 0u;
+        int done = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        // unrolled over the ring: every address is a constant away from a base
+        while (ok && done < nk) {
+#pragma unroll
+            for (int s = 0; s < S::kStages; ++s) {
+                if (!ok || done == nk) break;
+                // a full stage also says that the MMAs of its last use, and so the
+                // last readers of its scale slot, have completed
+                if (!mx4::warp_wait(&bars.full[s], ph, abort_flag, P.hdr)) {
+                    ok = false;
+                    break;
                 }
                 tc_fence_after();
                 const uint32_t st = base + s * S::kStage;
-                const uint32_t sfa = tmem + BN + (done & 1) * 16, sfb = sfa + 8;
+                const uint32_t sfa = tmem + BN + s * 16, sfb = sfa + 8;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    mx4::cp_sf<1>(sfa + 4 * h, mx4::sf_desc(st + S::kA + S::kB + h * mx4::kSfTile));
-                    mx4::cp_sf<1>(sfb + 4 * h, mx4::sf_desc(st + S::kA + S::kB + S::kSf + h * mx4::kSfTile));
+                    mx4::cp_sf<1>(one, sfa + 4 * h, mx4::sf_desc(st + S::kA + S::kB + h * mx4::kSfTile));
+                    mx4::cp_sf<1>(one, sfb + 4 * h, mx4::sf_desc(st + S::kA + S::kB + S::kSf + h * mx4::kSfTile));
                 }
                 const int steps = k0 + done == P.k_stages - 1 ? P.last_steps : 4;
-                for (int k = 0; k < steps; ++k) {
-                    const int id = (k & 1) * 2;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= steps) break;
+                    const uint32_t id = (k & 1) * 2;
                     const uint32_t col = (uint32_t)(k >> 1) * 4;
-                    mx4::mma<1>(tmem, mx4::operand_desc(st, k), mx4::operand_desc(st + S::kA, k),
-                                id ? mx4::idesc(kBM, BN, 2) : mx4::idesc(kBM, BN, 0),
-                                (sfa + col) | ((uint32_t)id << 30), (sfb + sfb_half + col) | ((uint32_t)id << 30),
-                                (done | k) != 0);
+                    mx4::mma<1>(one, tmem, mx4::operand_desc(st, k), mx4::operand_desc(st + S::kA, k),
+                                mx4::idesc(kBM, BN, (k & 1) * 2), (sfa + col) | (id << 30),
+                                (sfb + sfb_half + col) | (id << 30), (done | k) != 0);
                 }
-                mma_commit(&bars.empty[s]);
+                mx4::commit_one(one, &bars.empty[s]);
+                ++done;
             }
-            mma_commit(&bars.acc);
-            mbar_wait_drain(&bars.acc, 0, P.hdr);
-            tc_fence_before();
+            ph ^= 1;
         }
+        mx4::commit_one(one, &bars.acc);
+        mbar_wait_drain(&bars.acc, 0, P.hdr);
+        tc_fence_before();
     }
     __syncwarp();
     // every MMA and copy of this CTA has ended (or its bounded wait has):
@@ -189,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm(const __grid_constant__ Mx4
         }
         tc_fence_before();
     }
-    const int rows = min(kBM, P.m - m0), cols = min(BN, P.n - n0);
+    const int rows = min(kBM, P.m - m0);
     bool skip = bad;
     if (split > 1) {
         mx4::cluster_sync();
@@ -197,38 +180,9 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm(const __grid_constant__ Mx4
     } else {
         __syncthreads();
     }
-    if (!skip) {
-        const int stride = split * kThreads;
-        const int vec = (P.n & 3) == 0 ? 4 : 1;
-        // every rank stores its share of the tile
-        for (int u = rank * kThreads + threadIdx.x; u < rows * (BN / vec); u += stride) {
-            const int r = u / (BN / vec), c = (u % (BN / vec)) * vec;
-            if (c >= cols) continue;
-            const uint32_t at = smem_u32(part + r * S::kPitch + (c & ~3));
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (split == 1) {
-                v = *reinterpret_cast<const float4*>(part + r * S::kPitch + (c & ~3));
-            } else {
-                for (int q = 0; q < split; ++q) {
-                    const float4 p = mx4::ld_cluster4(mx4::map_rank(at, q));
-                    v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
-                }
-            }
-            const int64_t o = (int64_t)(m0 + r) * P.n + n0 + c;
-            if (vec == 4) {
-                if (P.bias) {
-                    const float* b = P.bias + n0 + c;
-                    v.x += b[0]; v.y += b[1]; v.z += b[2]; v.w += b[3];
-                }
-                store4_out(P, o, v);
-            } else {
-                const int t = c & 3;
-                float e = t == 0 ? v.x : (t == 1 ? v.y : (t == 2 ? v.z : v.w));
-                if (P.bias) e += P.bias[n0 + c];
-                store1_out(P, o, e);
-            }
-        }
-    }
+    // every rank stores its share of the tile
+    if (!skip)
+        mx4::store_partials<BN, S::kPitch>(P, part, m0, n0, rows, rank * kThreads + threadIdx.x, split * kThreads, split);
     // no CTA leaves while another reads its partial tile
     if (split > 1) mx4::cluster_sync();
     else __syncthreads();
@@ -279,13 +233,24 @@ bool mx4_operand_maps(CUtensorMap* codes_map, CUtensorMap* scales_map, const uin
                      words * 4, 256, (uint32_t)sf_tiles, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// The result in boxes of 128 bytes x 32 rows.
+bool mx4_out_map(CUtensorMap* map, void* out, int64_t m, int64_t n, int bf16) {
+    const uint64_t elem = bf16 ? 2 : 4;
+    return encode_2d(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, out, (uint64_t)n,
+                     (uint64_t)m, (uint64_t)n * elem, (uint32_t)(128 / elem), 32, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 namespace {
 
 template <int BN>
 cudaError_t launch(Mx4Params& P, int64_t m, int64_t n, int64_t k, const uint8_t* ac, const uint8_t* as,
                    const uint8_t* bc, const uint8_t* bs, int split, cudaStream_t st) {
     using S = Shape<BN>;
-    if (k > 0 && (!mx4_operand_maps(&P.ta, &P.tsa, ac, as, m, k, kBM, 1) ||
+    // fewer rows than a tile: only those (in eights) are brought in; the other
+    // rows of the stage hold anything, and so do their unused sums
+    const int box = m < kBM ? (int)(m + 7) / 8 * 8 : kBM;
+    const uint32_t stage_bytes = S::kStage - (uint32_t)(kBM - box) * 128;
+    if (k > 0 && (!mx4_operand_maps(&P.ta, &P.tsa, ac, as, m, k, box, 1) ||
                   !mx4_operand_maps(&P.tb, &P.tsb, bc, bs, n, k, BN, 1)))
         return cudaErrorInvalidValue;
     const int64_t n_tiles = (n + BN - 1) / BN, tiles = (m + kBM - 1) / kBM * n_tiles;
@@ -304,9 +269,59 @@ cudaError_t launch(Mx4Params& P, int64_t m, int64_t n, int64_t k, const uint8_t*
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     prof_begin(st);
-    e = cudaLaunchKernelEx(&cfg, mx4_gemm<BN>, P, (int)n_tiles, split);
+    e = cudaLaunchKernelEx(&cfg, mx4_gemm<BN>, P, (int)n_tiles, split, stage_bytes);
     prof_end(st, K_MX4_GEMM);
     return e;
+}
+
+}  // namespace
+
+namespace {
+
+struct Plan {
+    bool pair;
+    int bn, split;
+};
+
+// The kernel, tile width and split of the contraction with the least
+// estimated time: rounds of the tiles over the device x (steps of 256 columns
+// x time of one + time of a tile's end), with times measured on a B200:
+//   pair, 256 x 256     0.27 us a step, 1.0 us between tiles
+//   pair, 256 x 128     0.21, 0.7
+//   one CTA, 128 x 128  0.20, 2.5   (its end is not overlapped with a next tile)
+//   one CTA, 128 x 64   0.20, 1.5;  a split adds 0.6
+// and 148, 74, 33 and 15 clusters of 1, 2, 4 and 8 CTAs resident at a time (16:
+// 7, slower wherever it was tried).  Measured, in us (pair 256 / pair 128 /
+// best one-CTA form):
+//   8192 x 8192 x 8192    177 / 212 / 441     2048 x 1024 x 1024   6.6 / 5.9 / 7.7
+//   222283 x 4096 x 1024  457 / 514 / 3200    4999 x 1032 x 2008  13.8 / 14.0 / 27
+//   512 x 512 x 65536     76 / 52 / 19 (64 wide, split 4)
+//   1024 x 1024 x 65536   77 / 55 / 35 (128 wide, split 2)
+// Up to 128 rows the one-CTA form always wins (1 x 4096 x 1024: 5.5 / 5.4 /
+// 4.2, 1 x 8192 x 8192: 18 / 17 / 7.9): it fetches only the rows there are.
+Plan choose(int64_t m, int64_t n, int64_t steps, int sms) {
+    Plan best{false, 64, 1};
+    double least = 1e300;
+    auto consider = [&](bool pair, int bn, int split, double step, double end) {
+        const int bm = pair ? 256 : kBM;
+        const int64_t tiles = ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
+        const int64_t slots = pair ? sms / 2 : (split <= 2 ? sms / split : (split == 4 ? sms * 33 / 148 : sms * 15 / 148));
+        const int64_t rounds = (tiles + slots - 1) / slots;
+        const double t = (double)rounds * ((double)((steps + split - 1) / split) * step + end);
+        if (t < least) {
+            least = t;
+            best = Plan{pair, bn, split};
+        }
+    };
+    if (m > kBM && steps > 0) {
+        consider(true, 256, 1, 0.27, 1.0);
+        consider(true, 128, 1, 0.21, 0.7);
+    }
+    for (int split = 1; split <= 8 && (split == 1 || split <= steps); split *= 2) {
+        consider(false, 64, split, 0.20, split > 1 ? 2.1 : 1.5);
+        consider(false, 128, split, 0.20, split > 1 ? 3.1 : 2.5);
+    }
+    return best;
 }
 
 }  // namespace
@@ -327,13 +342,10 @@ cudaError_t mx4_product(int64_t m, int64_t n, int64_t k, const uint8_t* ac, cons
     P.hdr = hdr;
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t mt = (m + kBM - 1) / kBM;
-    const bool narrow = mt * ((n + 127) / 128) < sms;
-    const int64_t tiles = mt * (narrow ? (n + 63) / 64 : (n + 127) / 128);
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= sms && split * 2 <= P.k_stages) split *= 2;
-    return narrow ? launch<64>(P, m, n, k, ac, as, bc, bs, split, st)
-                  : launch<128>(P, m, n, k, ac, as, bc, bs, split, st);
+    const Plan plan = choose(m, n, P.k_stages, sms);
+    if (plan.pair) return mx4_product_pair(P, m, n, k, ac, as, bc, bs, plan.bn, sms, st);
+    return plan.bn == 64 ? launch<64>(P, m, n, k, ac, as, bc, bs, plan.split, st)
+                         : launch<128>(P, m, n, k, ac, as, bc, bs, plan.split, st);
 }
 
 }  // namespace jfa

@@ -89,6 +89,8 @@ def lib_path() -> str:
 def load():
     """Loads libjfa.so (building it if absent) and declares the signatures."""
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _LOCK:
         if _LIB is not None:
             return _LIB
@@ -487,33 +489,61 @@ def attention_backward(problem, q, k, v, out, lse, dout, q_offsets, kv_offsets, 
 # ---------------------------------------------------------------------------
 
 _TORCH_DTYPE = {torch.float32: JFA_F32, torch.bfloat16: JFA_BF16}
+_F32, _U8 = (torch.float32,), (torch.uint8,)
+# the current stream's handle by device index, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _need(ok: bool, msg: str):
-    if not ok:
-        raise JfaError(JFA_ERR_INVALID_ARGUMENT, msg)
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _invalid(msg: str):
+    raise JfaError(JFA_ERR_INVALID_ARGUMENT, msg)
 
 
 def _tensor(t, name, shape, dtypes, device):
-    """A contiguous CUDA tensor of the shape, one of the dtypes and on the device, or an error."""
-    _need(isinstance(t, torch.Tensor), f"{name}: a torch tensor is needed")
-    _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    _need(t.dtype in dtypes, f"{name}: dtype {t.dtype} is not one of {dtypes}")
-    _need(t.is_cuda and (device is None or t.device == device), f"{name}: device {t.device}, expected {device or 'cuda'}")
-    _need(t.is_contiguous(), f"{name}: must be contiguous")
+    """A contiguous CUDA tensor of the shape, one of the dtypes and on the device, or an error.
+    (Messages are only built for an error: these checks run before every small launch.)"""
+    if not isinstance(t, torch.Tensor):
+        _invalid(f"{name}: a torch tensor is needed")
+    if t.shape != shape:
+        _invalid(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        _invalid(f"{name}: dtype {t.dtype} is not one of {dtypes}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        _invalid(f"{name}: device {t.device}, expected {device or 'cuda'}")
+    if not t.is_contiguous():
+        _invalid(f"{name}: must be contiguous")
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """The tensors' device, and the stream the call and its results belong to."""
-    with torch.cuda.device(device):
-        if stream is None or isinstance(stream, torch.cuda.Stream):
-            s = stream or torch.cuda.current_stream(device)
-        else:
-            s = torch.cuda.ExternalStream(int(stream), device=device)
-        _need(s.device == device, f"stream of {s.device} for tensors of {device}")
-        with torch.cuda.stream(s):
-            yield s
+class _on:
+    """Makes the tensors' device current, and ``stream`` (default: the device's
+    current one) the stream that results are allocated on; enters as its handle."""
+    __slots__ = ("device", "stream", "stack")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.stack = device, stream, None
+
+    def __enter__(self):
+        dev, s = self.device, self.stream
+        if s is None and torch.cuda.current_device() == dev.index:
+            return _raw_stream(dev.index)
+        if s is not None and not isinstance(s, torch.cuda.Stream):
+            s = torch.cuda.ExternalStream(int(s), device=dev)
+        if s is not None and s.device != dev:
+            _invalid(f"stream of {s.device} for tensors of {dev}")
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(dev))
+        if s is not None:
+            self.stack.enter_context(torch.cuda.stream(s))
+        return torch.cuda.current_stream(dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.__exit__(*exc)
+        return False
 
 
 def mxfp4_workspace(device) -> torch.Tensor:
@@ -525,29 +555,37 @@ def quantize_mxfp4(x, along_rows=False, want_dequant=False, stream=None):
     """MXFP4 operand of ``x`` [rows, cols] (bf16 or fp32), or of its transpose
     with ``along_rows`` (blocks of 32 rows).  With ``want_dequant`` also
     returns the values it stands for, laid out like ``x``."""
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2, "x: a 2-D torch tensor is needed")
-    _tensor(x, "x", x.shape, tuple(_TORCH_DTYPE), None)
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        _invalid("x: a 2-D torch tensor is needed")
+    _tensor(x, "x", x.shape, _TORCH_DTYPE, None)
     rows, cols = x.shape
     r, c = (cols, rows) if along_rows else (rows, cols)
-    with _on(x.device, stream) as s:
-        u8 = dict(dtype=torch.uint8, device=x.device)
-        codes = torch.empty(r, (c + 31) // 32 * 16, **u8)
-        scales = torch.empty(jfa_mxfp4_scale_bytes(r, c), **u8)
+    dev, dt = x.device, _TORCH_DTYPE[x.dtype]
+    with _on(dev, stream) as s:
+        codes = torch.empty((r, (c + 31) // 32 * 16), dtype=torch.uint8, device=dev)
+        scales = torch.empty(_scale_bytes(r, c), dtype=torch.uint8, device=dev)
         if want_dequant:
             dequant = torch.empty_like(x)
-            jfa_quantize_mxfp4_dequant(x, _TORCH_DTYPE[x.dtype], rows, cols, along_rows, codes,
-                                       scales, dequant, stream=s)
+            _check(load().jfa_quantize_mxfp4_dequant(
+                x.data_ptr(), dt, rows, cols, 1 if along_rows else 0, codes.data_ptr(),
+                scales.data_ptr(), dequant.data_ptr(), s))
             return MxOperand(codes, scales, r, c), dequant
-        jfa_quantize_mxfp4(x, _TORCH_DTYPE[x.dtype], rows, cols, along_rows, codes, scales, stream=s)
+        _check(load().jfa_quantize_mxfp4(x.data_ptr(), dt, rows, cols, 1 if along_rows else 0,
+                                         codes.data_ptr(), scales.data_ptr(), s))
         return MxOperand(codes, scales, r, c)
 
 
+def _scale_bytes(rows, cols):
+    return (rows + 127) // 128 * ((cols + 127) // 128) * 512
+
+
 def _operand(o, name, device=None):
-    _need(isinstance(o, MxOperand), f"{name}: an MxOperand is needed")
-    _need(o.rows >= 0 and o.cols >= 0, f"{name}: negative size")
-    _tensor(o.codes, f"{name}.codes", (o.rows, (o.cols + 31) // 32 * 16), (torch.uint8,), device)
-    _tensor(o.scales, f"{name}.scales", (jfa_mxfp4_scale_bytes(o.rows, o.cols),), (torch.uint8,),
-            o.codes.device)
+    if not isinstance(o, MxOperand):
+        _invalid(f"{name}: an MxOperand is needed")
+    if o.rows < 0 or o.cols < 0:
+        _invalid(f"{name}: negative size")
+    _tensor(o.codes, name + ".codes", (o.rows, (o.cols + 31) // 32 * 16), _U8, device)
+    _tensor(o.scales, name + ".scales", (_scale_bytes(o.rows, o.cols),), _U8, o.codes.device)
 
 
 def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torch.bfloat16,
@@ -559,22 +597,28 @@ def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torc
     _operand(a, "a")
     dev = a.codes.device
     _operand(b, "b", dev)
-    _need(a.cols == b.cols, f"a has {a.cols} columns, b {b.cols}")
     m, n, k = a.rows, b.rows, a.cols
+    if k != b.cols:
+        _invalid(f"a has {k} columns, b {b.cols}")
     if bias is not None:
-        _tensor(bias, "bias", (n,), (torch.float32,), dev)
-    _need(out is not None or not accumulate, "accumulate needs out")
-    _need(out_dtype in _TORCH_DTYPE, f"out_dtype {out_dtype} is not one of {tuple(_TORCH_DTYPE)}")
+        _tensor(bias, "bias", (n,), _F32, dev)
     if out is not None:
-        _tensor(out, "out", (m, n), tuple(_TORCH_DTYPE), dev)
+        _tensor(out, "out", (m, n), _TORCH_DTYPE, dev)
+    elif accumulate:
+        _invalid("accumulate needs out")
+    elif out_dtype not in _TORCH_DTYPE:
+        _invalid(f"out_dtype {out_dtype} is not one of {tuple(_TORCH_DTYPE)}")
+    if ws is not None and (not ws.is_cuda or ws.device != dev):
+        _invalid(f"ws: device {ws.device}, expected {dev}")
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty(m, n, dtype=out_dtype, device=dev)
+            out = torch.empty((m, n), dtype=out_dtype, device=dev)
         if ws is None:
             ws = mxfp4_workspace(dev)
-        _need(ws.device == dev, f"ws: device {ws.device}, expected {dev}")
-        jfa_matmul_mxfp4(m, n, k, a.codes, a.scales, b.codes, b.scales, bias, out,
-                         _TORCH_DTYPE[out.dtype], accumulate, ws, stream=s)
+        _check(load().jfa_matmul_mxfp4(
+            m, n, k, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
+            b.scales.data_ptr(), _ptr(bias), out.data_ptr(), _TORCH_DTYPE[out.dtype],
+            1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), s))
         if check:
             jfa_check_error(ws, s)
     return out
@@ -593,13 +637,14 @@ def linear_mxfp4_backward(dy, x, w_t: MxOperand, dw=None, ws=None, stream=None, 
     product of operands quantised along its own contraction (the quantiser is
     passed straight through).  ``w_t``: ``quantize_mxfp4(weight,
     along_rows=True)``.  The bias's gradient is ``dy.sum(0)``."""
-    _need(isinstance(dy, torch.Tensor) and isinstance(x, torch.Tensor) and dy.dim() == 2
-          and x.dim() == 2 and dy.shape[0] == x.shape[0], "dy [m, n] and x [m, k] are needed")
+    if not (isinstance(dy, torch.Tensor) and isinstance(x, torch.Tensor) and dy.dim() == 2
+            and x.dim() == 2 and dy.shape[0] == x.shape[0]):
+        _invalid("dy [m, n] and x [m, k] are needed")
     _operand(w_t, "w_t")
-    _need(w_t.rows == x.shape[1] and w_t.cols == dy.shape[1],
-          f"w_t is {w_t.rows} x {w_t.cols}, expected {x.shape[1]} x {dy.shape[1]}")
+    if w_t.rows != x.shape[1] or w_t.cols != dy.shape[1]:
+        _invalid(f"w_t is {w_t.rows} x {w_t.cols}, expected {x.shape[1]} x {dy.shape[1]}")
     if dw is not None:
-        _tensor(dw, "dw", (dy.shape[1], x.shape[1]), (torch.float32,), dy.device)
+        _tensor(dw, "dw", (dy.shape[1], x.shape[1]), _F32, dy.device)
     if ws is None:
         with _on(dy.device, stream):
             ws = mxfp4_workspace(dy.device)
@@ -619,14 +664,18 @@ def block_norm_workspace(desc: jfa_block_norm, device) -> torch.Tensor:
 
 
 def _block_norm_args(desc, x, tensors, params):
-    _need(isinstance(x, torch.Tensor), "x: a torch tensor is needed")
-    dt = tuple(d for d, code in _TORCH_DTYPE.items() if code == desc.dtype)
-    for name, t in [("x", x)] + list(tensors.items()):
+    if not isinstance(x, torch.Tensor):
+        _invalid("x: a torch tensor is needed")
+    dt = (torch.bfloat16,) if desc.dtype == JFA_BF16 else _F32
+    dim, dev = desc.dim, x.device
+    shape = (desc.rows, dim)
+    _tensor(x, "x", shape, dt, None)
+    for name, t in tensors.items():
         if t is not None:
-            _tensor(t, name, (desc.rows, desc.dim), dt, x.device)
+            _tensor(t, name, shape, dt, dev)
     for name, t in params.items():
         if t is not None:
-            _tensor(t, name, (desc.dim,), (torch.float32,), x.device)
+            _tensor(t, name, (dim,), _F32, dev)
 
 
 def block_norm_forward(desc: jfa_block_norm, x, block, gate=None, scale=None, post_gamma=None,
@@ -639,7 +688,10 @@ def block_norm_forward(desc: jfa_block_norm, x, block, gate=None, scale=None, po
     with _on(x.device, stream) as s:
         y = torch.empty_like(x)
         n = torch.empty_like(x) if desc.pre_norm != NORM["none"] else None
-        jfa_block_norm_forward(desc, x, block, gate, *params.values(), y, n, stream=s)
+        _check(load().jfa_block_norm_forward(
+            ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), _ptr(scale),
+            _ptr(post_gamma), _ptr(post_beta), _ptr(pre_gamma), _ptr(pre_beta), y.data_ptr(),
+            _ptr(n), s))
     return y, n
 
 
@@ -655,10 +707,13 @@ def block_norm_backward(desc: jfa_block_norm, x, block, gate=None, scale=None, p
     with _on(x.device, stream) as s:
         if ws is None:
             ws = block_norm_workspace(desc, x.device)
-        _need(ws.device == x.device, f"ws: device {ws.device}, expected {x.device}")
+        elif ws.device != x.device:
+            _invalid(f"ws: device {ws.device}, expected {x.device}")
         g = {"x": torch.empty_like(x), "block": torch.empty_like(x),
              "gate": None if gate is None else torch.empty_like(x)}
         g.update({k: None if p is None else torch.empty_like(p) for k, p in params.items()})
-        jfa_block_norm_backward(desc, x, block, gate, *params.values(), dy, dn, *g.values(), ws,
-                                stream=s)
+        _check(load().jfa_block_norm_backward(
+            ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), _ptr(scale),
+            _ptr(post_gamma), _ptr(post_beta), _ptr(pre_gamma), _ptr(pre_beta), _ptr(dy), _ptr(dn),
+            *map(_ptr, g.values()), ws.data_ptr(), ws.numel() * ws.element_size(), s))
     return g

@@ -17,21 +17,35 @@
 // kept between the passes.  All arithmetic and sums are fp32; each result is
 // rounded once.
 //
+// With S1 = sum_rows d * act(u) * hat and S2 = sum_rows d * act(u) of the
+// block's norm the parameter gradients are dgamma_post = s S1, dbeta_post = s S2
+// and ds = gamma S1 + beta S2, so two sums (one without a LayerNorm) serve all
+// three; the same pair without the gate serves N_pre's.
+//
 // Bound: HBM.  Forward 3 tensors read and 2 written, backward 5 read and 3
-// written.  A row is read once into the registers of a group of threads
-// (eight elements per thread and tensor), and all statistics are taken from
-// there; centred sums, so that a large mean costs no digits.  The parameter
-// gradients are summed per thread over the rows a CTA takes, written as one
-// partial row per CTA and summed in a fixed order by a second small kernel:
-// no atomics, the same result every time.
+// written.  Persistent groups of threads take rows in turn, a row's values in
+// registers, one 16-byte vector per thread, tensor and chunk; the next row's
+// vectors are loaded before the current row is worked on, and the parameters
+// stay in registers.  Statistics are taken from the registers: centred sums, so
+// that a large mean costs no digits.  Parameter gradients are summed per thread
+// over the group's rows, written as one partial row per CTA and summed in a
+// fixed order by a second small kernel: no atomics, the same result every time.
+//
+// Rows of any width go in aligned vectors: a row that starts s elements behind
+// a 16-byte boundary is taken from that boundary on, the elements of its
+// neighbours masked.  s repeats every 16 / sizeof(element) rows, and a group's
+// rows are a multiple of that apart, so that a thread keeps the same columns
+// (and its parameters and sums) for all its rows.
 #include "jfa_common.cuh"
+#include "jfa_sm100.cuh"
 
 namespace jfa {
 
 namespace {
 
-constexpr int kE = 8;              // elements per thread, chunk and tensor
 constexpr int kMaxDim = 8192;
+constexpr int kMaxThreads = 512;   // per row; wider rows take several vectors per thread
+constexpr int kSmallThreads = 128; // CTA size for rows within a warp
 constexpr int kMaxParts = 1184;    // partial rows of the backward: 8 CTAs on each of 148 SMs
 
 struct NormArgs {
@@ -40,7 +54,7 @@ struct NormArgs {
     const void *dy, *dn;
     void *y, *n;                   // forward results
     void *dx, *dblock, *dgate;     // backward results
-    float* parts;                  // [grid][5][D]
+    float* parts;                  // [grid][Q_COUNT][D]
     int64_t rows;
     int D, post, pre, gate_kind;
     float eps;
@@ -53,12 +67,17 @@ struct Group {
     int warps;         // 1: within a warp
     float2* buf;       // [2][32]
     int turn;
-    // sums of a and b over the group, in every thread
+    __device__ __forceinline__ Group(int G_, float2* b) : G(G_), t(threadIdx.x % G_), warps(G_ <= 32 ? 1 : G_ / 32), buf(b), turn(0) {}
+    // sums of a (and b) over the group, in every thread
+    template <bool TWO>
     __device__ __forceinline__ float2 sum(float a, float b) {
         const int width = G < 32 ? G : 32;
-        for (int o = width >> 1; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            if (o < width) {
+                a += __shfl_xor_sync(0xffffffffu, a, o);
+                if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
+            }
         }
         if (warps == 1) return make_float2(a, b);
         // alternating buffers: one barrier per sum
@@ -66,420 +85,508 @@ struct Group {
         ++turn;
         if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = make_float2(a, b);
         __syncthreads();
-        float2 s = make_float2(0.f, 0.f);
-        for (int w = 0; w < warps; ++w) {
-            s.x += p[w].x;
-            s.y += p[w].y;
+        float2 s = p[0];
+        for (int w = 1; w < warps; ++w) {
+            const float2 q = p[w];
+            s.x += q.x;
+            if (TWO) s.y += q.y;
         }
         return s;
     }
 };
 
-// Column of element u of chunk ch: eight consecutive columns per thread when
-// rows are 16-byte aligned (VEC), else columns G apart, so that a warp's
-// access is 32 consecutive elements.
-template <bool VEC>
-__device__ __forceinline__ int column(const Group& g, int ch, int u) {
-    return VEC ? (ch * g.G + g.t) * kE + u : (ch * kE + u) * g.G + g.t;
-}
+// Values are kept in pairs: the paired fp32 instructions do two elements at
+// once, and these kernels are close to being bound by issue.
+using sm100::add2;
+using sm100::fma2;
+using sm100::mul2;
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-template <bool VEC>
-__device__ __forceinline__ void load_row(const float* p, const Group& g, int ch, int D, float (&f)[kE]) {
-    if (VEC) {
-        const int c = column<VEC>(g, ch, 0);
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        if (c < D) {
-            a = __ldg(reinterpret_cast<const float4*>(p + c));
-            b = __ldg(reinterpret_cast<const float4*>(p + c) + 1);
-        }
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else {
-#pragma unroll
-        for (int u = 0; u < kE; ++u) {
-            const int c = column<VEC>(g, ch, u);
-            f[u] = c < D ? __ldg(p + c) : 0.f;
-        }
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    __device__ static __forceinline__ void unpack(const uint4& r, float2* f) {
+        f[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+        f[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
     }
-}
-template <bool VEC>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, const Group& g, int ch, int D, float (&f)[kE]) {
-    if (VEC) {
-        const int c = column<VEC>(g, ch, 0);
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (c < D) raw = __ldg(reinterpret_cast<const uint4*>(p + c));
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            f[2 * u] = __uint_as_float(w[u] << 16);
-            f[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < kE; ++u) {
-            const int c = column<VEC>(g, ch, u);
-            f[u] = c < D ? __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p + c)) << 16) : 0.f;
-        }
+    __device__ static __forceinline__ uint4 pack(const float2* f) {
+        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
     }
-}
-template <bool VEC>
-__device__ __forceinline__ void store_row(float* p, const Group& g, int ch, int D, const float (&f)[kE]) {
-    if (VEC) {
-        const int c = column<VEC>(g, ch, 0);
-        if (c < D) {
-            reinterpret_cast<float4*>(p + c)[0] = make_float4(f[0], f[1], f[2], f[3]);
-            reinterpret_cast<float4*>(p + c)[1] = make_float4(f[4], f[5], f[6], f[7]);
-        }
-    } else {
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static __forceinline__ void unpack(const uint4& r, float2* f) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int u = 0; u < kE; ++u) {
-            const int c = column<VEC>(g, ch, u);
-            if (c < D) p[c] = f[u];
-        }
+        for (int u = 0; u < 4; ++u) f[u] = make_float2(__uint_as_float(w[u] << 16), __uint_as_float(w[u] & 0xFFFF0000u));
     }
-}
-template <bool VEC>
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, const Group& g, int ch, int D, const float (&f)[kE]) {
-    if (VEC) {
-        const int c = column<VEC>(g, ch, 0);
-        if (c < D) {
-            uint4 o;
-            __nv_bfloat162* w = reinterpret_cast<__nv_bfloat162*>(&o);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) w[u] = __floats2bfloat162_rn(f[2 * u], f[2 * u + 1]);
-            *reinterpret_cast<uint4*>(p + c) = o;
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < kE; ++u) {
-            const int c = column<VEC>(g, ch, u);
-            if (c < D) p[c] = __float2bfloat16_rn(f[u]);
-        }
+    __device__ static __forceinline__ uint4 pack(const float2* f) {
+        return make_uint4(sm100::pack_bf16(f[0].x, f[0].y), sm100::pack_bf16(f[1].x, f[1].y),
+                          sm100::pack_bf16(f[2].x, f[2].y), sm100::pack_bf16(f[3].x, f[3].y));
     }
-}
-// A parameter vector's values (a constant where it is absent).
-template <bool VEC>
-__device__ __forceinline__ void load_param(const float* p, float absent, const Group& g, int ch, int D, float (&f)[kE]) {
-    if (p) {
-        load_row<VEC>(p, g, ch, D, f);
-    } else {
-#pragma unroll
-        for (int u = 0; u < kE; ++u) f[u] = absent;
-    }
-}
+};
 
-// 1 / (1 + e^-u): a large negative u gives 0.
-__device__ __forceinline__ float sigmoid(float u) { return __fdividef(1.0f, 1.0f + expf(-u)); }
-
-__device__ __forceinline__ float gate_value(int kind, float u) {
-    if (kind == JFA_GATE_NONE) return 1.0f;
-    if (kind == JFA_GATE_IDENTITY) return u;
-    const float s = sigmoid(u);
-    return kind == JFA_GATE_SILU ? u * s : s;
-}
-
-// Turns v into (v - mu) * r in place and returns r.
-template <bool VEC, int NCH>
-__device__ __forceinline__ float normalise(float (&v)[NCH][kE], int kind, Group& g, int D, float eps) {
-    if (kind == JFA_NORM_LAYER) {
-        float s = 0.f;
+// A thread's columns of its group's rows: vector (ch * G + t) from the aligned
+// start, `shift` elements before column 0.
+template <typename T, int NCH>
+struct Cols {
+    static constexpr int V = Vec<T>::N;
+    static constexpr int P = NCH * V / 2;   // pairs
+    int D, c0, step;   // c0: column of the first element of chunk 0; chunks are `step` apart
+    bool clean;        // every element of every chunk lies in the row
+    int64_t total;
+    __device__ __forceinline__ Cols(int D_, int64_t rows, int64_t row, const Group& g)
+        : D(D_), c0(g.t * V - (int)((row * D_) % V)), step(g.G * V), total(rows * D_) {
+        clean = true;
 #pragma unroll
-        for (int ch = 0; ch < NCH; ++ch)
-#pragma unroll
-            for (int u = 0; u < kE; ++u) s += v[ch][u];
-        const float mu = g.sum(s, 0.f).x / (float)D;   // exact for a constant row of exact sum
-#pragma unroll
-        for (int ch = 0; ch < NCH; ++ch)
-#pragma unroll
-            for (int u = 0; u < kE; ++u) v[ch][u] = column<VEC>(g, ch, u) < D ? v[ch][u] - mu : 0.f;
+        for (int ch = 0; ch < NCH; ++ch) clean = clean && full(ch);
     }
-    float q = 0.f;
+    __device__ __forceinline__ int first(int ch) const { return c0 + ch * step; }
+    __device__ __forceinline__ bool any(int ch) const { return first(ch) < D && first(ch) + V > 0; }
+    __device__ __forceinline__ bool full(int ch) const { return first(ch) >= 0 && first(ch) + V <= D; }
+    __device__ __forceinline__ bool in(int ch, int u) const { return (unsigned)(first(ch) + u) < (unsigned)D; }
+
+    // `at`: offset of the row's column 0
+    __device__ __forceinline__ uint4 load(const void* base, int64_t at, int ch) const {
+        if (!any(ch)) return make_uint4(0u, 0u, 0u, 0u);
+        const T* p = reinterpret_cast<const T*>(base) + (at + first(ch));
+        if (at + first(ch) + V <= total) return __ldg(reinterpret_cast<const uint4*>(p));
+        // the tensor ends inside this vector
+        uint4 r = make_uint4(0u, 0u, 0u, 0u);
+        T* e = reinterpret_cast<T*>(&r);
 #pragma unroll
-    for (int ch = 0; ch < NCH; ++ch)
+        for (int u = 0; u < V; ++u)
+            if (in(ch, u)) e[u] = p[u];
+        return r;
+    }
+    // elements outside the row (a neighbour's, or nothing) to zero
+    __device__ __forceinline__ void mask(float2 (&f)[P]) const {
+        if (clean) return;
 #pragma unroll
-        for (int u = 0; u < kE; ++u) q = fmaf(v[ch][u], v[ch][u], q);
-    const float r = 1.0f / sqrtf(g.sum(q, 0.f).x / (float)D + eps);
+        for (int i = 0; i < P; ++i) {
+            if (!in(2 * i / V, 2 * i % V)) f[i].x = 0.f;
+            if (!in(2 * i / V, 2 * i % V + 1)) f[i].y = 0.f;
+        }
+    }
+    __device__ __forceinline__ void get(const uint4 (&r)[NCH], float2 (&f)[P]) const {
 #pragma unroll
-    for (int ch = 0; ch < NCH; ++ch)
+        for (int ch = 0; ch < NCH; ++ch) Vec<T>::unpack(r[ch], f + ch * V / 2);
+        mask(f);
+    }
+    __device__ __forceinline__ void store(void* base, int64_t at, const float2 (&f)[P]) const {
 #pragma unroll
-        for (int u = 0; u < kE; ++u) v[ch][u] *= r;
+        for (int ch = 0; ch < NCH; ++ch) {
+            T* p = reinterpret_cast<T*>(base) + (at + first(ch));
+            if (full(ch)) {
+                *reinterpret_cast<uint4*>(p) = Vec<T>::pack(f + ch * V / 2);
+            } else if (any(ch)) {
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+                    if (in(ch, u)) p[u] = from_f<T>(u & 1 ? f[(ch * V + u) / 2].y : f[(ch * V + u) / 2].x);
+            }
+        }
+    }
+    // a parameter vector's values (`absent` where there is none, 0 outside the row)
+    __device__ __forceinline__ float param(const float* p, float absent, int i) const {
+        const int ch = i / V, u = i % V;
+        return in(ch, u) ? (p ? __ldg(p + first(ch) + u) : absent) : 0.f;
+    }
+};
+
+// 1 / (1 + e^-u) with the hardware's base-2 exponential and reciprocal (a few
+// units in the last place, times 1 + |u| / 16 for the rounding of the scaled
+// argument); a large negative u gives 0.
+__device__ __forceinline__ float sigmoid(float u) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + sm100::ex2(u * -1.4426950408889634f)));
     return r;
 }
 
-__device__ __forceinline__ Group make_group(int G, float2* buf) {
-    Group g;
-    g.G = G;
-    g.t = threadIdx.x % G;
-    g.warps = G <= 32 ? 1 : G / 32;
-    g.buf = buf;
-    g.turn = 0;
-    return g;
+// act(u) in place and, SLOPE, act'(u).
+template <int P, bool SLOPE>
+__device__ __forceinline__ void gate_values(int kind, float2 (&u)[P], float2 (&slope)[SLOPE ? P : 1]) {
+    if (kind == JFA_GATE_SILU) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float2 q = make_float2(sigmoid(u[i].x), sigmoid(u[i].y)), v = u[i];
+            u[i] = mul2(v, q);
+            // q (1 + v (1 - q)) = q + v q - (v q) q
+            if (SLOPE) slope[SLOPE ? i : 0] = mul2(q, fma2(v, fma2(q, both(-1.f), both(1.f)), both(1.f)));
+        }
+    } else if (kind == JFA_GATE_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            u[i] = make_float2(sigmoid(u[i].x), sigmoid(u[i].y));
+            if (SLOPE) slope[SLOPE ? i : 0] = mul2(u[i], fma2(u[i], both(-1.f), both(1.f)));
+        }
+    } else if (kind == JFA_GATE_IDENTITY) {
+        if (SLOPE) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) slope[SLOPE ? i : 0] = both(1.f);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) u[i] = both(1.f);
+    }
 }
 
-// One row per group.  Threads of rows behind the last take part in the
-// shuffles with zeros and store nothing.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(1024) block_norm_fwd(const NormArgs a, int G) {
-    __shared__ float2 buf[64];
-    Group g = make_group(G, buf);
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
-    const bool live = row < a.rows;
-    const int D = live ? a.D : 0;   // a dead row reads and writes no column
-    const int64_t at = row * a.D;
-    float x[1][kE], b[1][kE], u[kE], w[kE], v[kE];
-    load_row<VEC>(reinterpret_cast<const T*>(a.block) + at, g, 0, D, b[0]);
-    load_row<VEC>(reinterpret_cast<const T*>(a.x) + at, g, 0, D, x[0]);
-    if (a.gate_kind != JFA_GATE_NONE) load_row<VEC>(reinterpret_cast<const T*>(a.gate) + at, g, 0, D, u);
-    if (a.post != JFA_NORM_NONE) {
-        normalise<VEC, 1>(b, a.post, g, a.D, a.eps);
-        load_param<VEC>(a.post_gamma, 1.f, g, 0, a.D, w);
-        load_param<VEC>(a.post_beta, 0.f, g, 0, a.D, v);
+// Turns v into (v - mu) * r in place (0 outside the row) and returns r.
+template <typename T, int NCH, bool LN>
+__device__ __forceinline__ float normalise(float2 (&v)[Cols<T, NCH>::P], int kind, const Cols<T, NCH>& cols, Group& g,
+                                           float inv_d, float eps) {
+    constexpr int P = Cols<T, NCH>::P;
+    if (LN && kind == JFA_NORM_LAYER) {
+        float2 s = v[0];
 #pragma unroll
-        for (int i = 0; i < kE; ++i) b[0][i] = fmaf(b[0][i], w[i], v[i]);
+        for (int i = 1; i < P; ++i) s = add2(s, v[i]);
+        const float mu = g.template sum<false>(s.x + s.y, 0.f).x / (float)cols.D;   // exact for a constant row of exact sum
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = add2(v[i], both(-mu));
+        cols.mask(v);
     }
-    load_param<VEC>(a.scale, 1.f, g, 0, a.D, w);
+    float2 q = mul2(v[0], v[0]);
 #pragma unroll
-    for (int i = 0; i < kE; ++i) {
-        const float k = a.gate_kind != JFA_GATE_NONE ? w[i] * gate_value(a.gate_kind, u[i]) : w[i];
-        x[0][i] = fmaf(k, b[0][i], x[0][i]);
-    }
-    store_row<VEC>(reinterpret_cast<T*>(a.y) + at, g, 0, D, x[0]);
-    if (a.pre == JFA_NORM_NONE) return;
-    normalise<VEC, 1>(x, a.pre, g, a.D, a.eps);
-    load_param<VEC>(a.pre_gamma, 1.f, g, 0, a.D, w);
-    load_param<VEC>(a.pre_beta, 0.f, g, 0, a.D, v);
+    for (int i = 1; i < P; ++i) q = fma2(v[i], v[i], q);
+    const float r = rsqrtf(fmaf(g.template sum<false>(q.x + q.y, 0.f).x, inv_d, eps));
 #pragma unroll
-    for (int i = 0; i < kE; ++i) x[0][i] = fmaf(x[0][i], w[i], v[i]);
-    store_row<VEC>(reinterpret_cast<T*>(a.n) + at, g, 0, D, x[0]);
+    for (int i = 0; i < P; ++i) v[i] = mul2(v[i], both(r));
+    return r;
 }
 
-enum { Q_SCALE = 0, Q_POST_GAMMA, Q_POST_BETA, Q_PRE_GAMMA, Q_PRE_BETA, Q_COUNT };
-
-// The sums over rows: in registers for one chunk, in shared memory (each
-// thread its own columns) for two, where registers run out.
-template <int NCH>
-struct Sums;
-template <>
-struct Sums<1> {
-    float v[Q_COUNT][kE];
-    __device__ void init(float*, const Group&, int) {
-#pragma unroll
-        for (int q = 0; q < Q_COUNT; ++q)
-#pragma unroll
-            for (int u = 0; u < kE; ++u) v[q][u] = 0.f;
-    }
-    __device__ __forceinline__ void add(int q, int, int u, float x) { v[q][u] += x; }
-    __device__ __forceinline__ float get(int q, int, int u) const { return v[q][u]; }
-};
-template <>
-struct Sums<2> {
-    float* mine;
-    int stride;
-    __device__ void init(float* smem, const Group& g, int) {
-        mine = smem + g.t;
-        stride = g.G;
-        for (int i = 0; i < Q_COUNT * 2 * kE; ++i) mine[i * stride] = 0.f;
-    }
-    __device__ __forceinline__ void add(int q, int ch, int u, float x) { mine[((q * 2 + ch) * kE + u) * stride] += x; }
-    __device__ __forceinline__ float get(int q, int ch, int u) const { return mine[((q * 2 + ch) * kE + u) * stride]; }
-};
-
-// A CTA takes rows blockIdx, blockIdx + gridDim, ... (in units of its groups).
-template <typename T, bool VEC, int NCH>
-__global__ void __launch_bounds__(512) block_norm_bwd(const NormArgs a, int G) {
-    extern __shared__ float smem[];   // NCH == 2: the sums; small groups: the CTA's reduction
+// LN: a norm is a LayerNorm, so that there may be betas.
+template <typename T, int NCH, bool LN>
+__global__ void __launch_bounds__(kMaxThreads) block_norm_fwd(const NormArgs a, int G) {
+    constexpr int P = Cols<T, NCH>::P;
     __shared__ float2 buf[64];
-    Group g = make_group(G, buf);
-    Sums<NCH> sums;
-    sums.init(smem, g, a.D);
+    Group g(G, buf);
     const int groups = blockDim.x / G;
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    int64_t base = (int64_t)blockIdx.x * groups, row = base + threadIdx.x / G;
+    const Cols<T, NCH> cols(a.D, a.rows, row, g);
+    const bool gated = a.gate_kind != JFA_GATE_NONE, pre = a.pre != JFA_NORM_NONE;
     const float inv_d = 1.0f / (float)a.D;
-    for (int64_t base = (int64_t)blockIdx.x * groups; base < a.rows; base += (int64_t)gridDim.x * groups) {
-        const int64_t row = base + threadIdx.x / G;
-        const int D = row < a.rows ? a.D : 0;
-        const int64_t at = row * a.D;
-        float b[NCH][kE], y[NCH][kE], u[NCH][kE], d[NCH][kE], dn[NCH][kE];
+    uint4 rb[NCH], rx[NCH], ru[NCH];
+    int64_t at = row * a.D, at_next = at;
+    auto fetch = [&](bool live) {
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
-            load_row<VEC>(reinterpret_cast<const T*>(a.block) + at, g, ch, D, b[ch]);
-            load_row<VEC>(reinterpret_cast<const T*>(a.x) + at, g, ch, D, y[ch]);
-            if (a.gate_kind != JFA_GATE_NONE) load_row<VEC>(reinterpret_cast<const T*>(a.gate) + at, g, ch, D, u[ch]);
-            load_row<VEC>(reinterpret_cast<const T*>(a.dy) + at, g, ch, D, d[ch]);
-            if (a.pre != JFA_NORM_NONE) load_row<VEC>(reinterpret_cast<const T*>(a.dn) + at, g, ch, D, dn[ch]);
-        }
-        float rb = 1.f;
-        if (a.post != JFA_NORM_NONE) rb = normalise<VEC, NCH>(b, a.post, g, a.D, a.eps);   // b: hat of the block
-        float gate[NCH][kE];   // act(u)
-        if (a.pre != JFA_NORM_NONE) {
-#pragma unroll
-            for (int ch = 0; ch < NCH; ++ch) {
-                float s[kE], pg[kE], pb[kE];
-                load_param<VEC>(a.scale, 1.f, g, ch, a.D, s);
-                load_param<VEC>(a.post_gamma, 1.f, g, ch, a.D, pg);
-                load_param<VEC>(a.post_beta, 0.f, g, ch, a.D, pb);
-#pragma unroll
-                for (int i = 0; i < kE; ++i) {
-                    gate[ch][i] = a.gate_kind != JFA_GATE_NONE ? gate_value(a.gate_kind, u[ch][i]) : 1.f;
-                    y[ch][i] = fmaf(s[i] * gate[ch][i], fmaf(b[ch][i], pg[i], pb[i]), y[ch][i]);
-                }
+            rb[ch] = rx[ch] = ru[ch] = make_uint4(0u, 0u, 0u, 0u);
+            if (live) {
+                rb[ch] = cols.load(a.block, at_next, ch);
+                rx[ch] = cols.load(a.x, at_next, ch);
+                if (gated) ru[ch] = cols.load(a.gate, at_next, ch);
             }
-            const float ry = normalise<VEC, NCH>(y, a.pre, g, a.D, a.eps);   // y: hat of y
-            float c1 = 0.f, c2 = 0.f;
-#pragma unroll
-            for (int ch = 0; ch < NCH; ++ch) {
-                float w[kE];
-                load_param<VEC>(a.pre_gamma, 1.f, g, ch, a.D, w);
-#pragma unroll
-                for (int i = 0; i < kE; ++i) {
-                    sums.add(Q_PRE_GAMMA, ch, i, dn[ch][i] * y[ch][i]);
-                    sums.add(Q_PRE_BETA, ch, i, dn[ch][i]);
-                    dn[ch][i] *= w[i];
-                    c1 = fmaf(dn[ch][i], y[ch][i], c1);
-                    c2 += dn[ch][i];
-                }
-            }
-            const float2 c = g.sum(c1, c2);
-            c1 = c.x * inv_d;
-            c2 = a.pre == JFA_NORM_LAYER ? c.y * inv_d : 0.f;
-#pragma unroll
-            for (int ch = 0; ch < NCH; ++ch)
-#pragma unroll
-                for (int i = 0; i < kE; ++i) d[ch][i] = fmaf(ry, dn[ch][i] - fmaf(y[ch][i], c1, c2), d[ch][i]);
-        } else {
-#pragma unroll
-            for (int ch = 0; ch < NCH; ++ch)
-#pragma unroll
-                for (int i = 0; i < kE; ++i) gate[ch][i] = a.gate_kind != JFA_GATE_NONE ? gate_value(a.gate_kind, u[ch][i]) : 1.f;
         }
-        // d is dx; with the block: dp, the gate's gradient and the sums
-        float c1 = 0.f, c2 = 0.f;
+    };
+    fetch(row < a.rows);
+    // y = x + act(u) * (w1 * hat + w0), n = hat_y * q1 + q0
+    float2 w1[P], w0[LN ? P : 1], q1[P], q0[LN ? P : 1];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const float2 s = make_float2(cols.param(a.scale, 1.f, 2 * i), cols.param(a.scale, 1.f, 2 * i + 1));
+        w1[i] = mul2(s, make_float2(cols.param(a.post_gamma, 1.f, 2 * i), cols.param(a.post_gamma, 1.f, 2 * i + 1)));
+        q1[i] = make_float2(cols.param(a.pre_gamma, 1.f, 2 * i), cols.param(a.pre_gamma, 1.f, 2 * i + 1));
+        if (LN) {
+            w0[LN ? i : 0] = mul2(s, make_float2(cols.param(a.post_beta, 0.f, 2 * i), cols.param(a.post_beta, 0.f, 2 * i + 1)));
+            q0[LN ? i : 0] = make_float2(cols.param(a.pre_beta, 0.f, 2 * i), cols.param(a.pre_beta, 0.f, 2 * i + 1));
+        }
+    }
+    for (; base < a.rows; base += stride, row += stride, at = at_next) {
+        float2 b[P], x[P], k[P], none[1];
+        cols.get(rb, b);
+        cols.get(rx, x);
+        cols.get(ru, k);
+        at_next = at + stride * a.D;
+        fetch(row + stride < a.rows);
+        if (a.post != JFA_NORM_NONE) normalise<T, NCH, LN>(b, a.post, cols, g, inv_d, a.eps);
+        if (gated) gate_values<P, false>(a.gate_kind, k, none);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float2 p = LN ? fma2(b[i], w1[i], w0[LN ? i : 0]) : mul2(b[i], w1[i]);
+            x[i] = gated ? fma2(k[i], p, x[i]) : add2(x[i], p);
+        }
+        const bool live = row < a.rows;
+        if (live) cols.store(a.y, at, x);
+        if (!pre) continue;
+        normalise<T, NCH, LN>(x, a.pre, cols, g, inv_d, a.eps);
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = LN ? fma2(x[i], q1[i], q0[LN ? i : 0]) : mul2(x[i], q1[i]);
+        if (live) cols.store(a.n, at, x);
+    }
+}
+
+enum { Q_POST1 = 0, Q_PRE1, Q_POST0, Q_PRE0, Q_COUNT };   // S1 of the two norms, S2 of the two
+
+// The sums over rows, in pairs: in registers, or in shared memory (each thread
+// its own columns) where a thread has so many elements that registers run out.
+template <int P, int Q, bool SMEM>
+struct Sums {
+    float2 v[Q][P];
+    __device__ __forceinline__ Sums(float*, const Group&) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[q][i] = both(0.f);
+    }
+    __device__ __forceinline__ void add(int q, int i, float2 x) { v[q][i] = add2(v[q][i], x); }
+    __device__ __forceinline__ void fma(int q, int i, float2 x, float2 y) { v[q][i] = fma2(x, y, v[q][i]); }
+    __device__ __forceinline__ float2 get(int q, int i) const { return v[q][i]; }
+};
+template <int P, int Q>
+struct Sums<P, Q, true> {
+    float2* mine;
+    int stride;
+    __device__ __forceinline__ Sums(float* smem, const Group& g) : mine(reinterpret_cast<float2*>(smem) + g.t), stride(g.G) {
+        for (int i = 0; i < Q * P; ++i) mine[i * stride] = both(0.f);
+    }
+    __device__ __forceinline__ void add(int q, int i, float2 x) {
+        float2& m = mine[(q * P + i) * stride];
+        m = add2(m, x);
+    }
+    __device__ __forceinline__ void fma(int q, int i, float2 x, float2 y) {
+        float2& m = mine[(q * P + i) * stride];
+        m = fma2(x, y, m);
+    }
+    __device__ __forceinline__ float2 get(int q, int i) const { return mine[(q * P + i) * stride]; }
+};
+
+template <typename T, int NCH, bool LN>
+__global__ void __launch_bounds__(kMaxThreads) block_norm_bwd(const NormArgs a, int G) {
+    constexpr int V = Vec<T>::N, P = Cols<T, NCH>::P, Q = LN ? 4 : 2;
+    constexpr bool kSmem = P > 4, kAhead = NCH == 1;
+    extern __shared__ float smem[];   // P > 4: the sums; small groups: the CTA's reduction
+    __shared__ float2 buf[64];
+    Group g(G, buf);
+    Sums<P, Q, kSmem> sums(smem, g);
+    const int groups = blockDim.x / G;
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    int64_t base = (int64_t)blockIdx.x * groups, row = base + threadIdx.x / G;
+    const Cols<T, NCH> cols(a.D, a.rows, row, g);
+    const bool gated = a.gate_kind != JFA_GATE_NONE, pre = a.pre != JFA_NORM_NONE;
+    const float inv_d = 1.0f / (float)a.D;
+    uint4 rb[NCH], rx[NCH], ru[NCH], rdy[NCH], rdn[NCH];
+    int64_t at = row * a.D, at_next = at;
+    auto fetch = [&](bool live) {
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
-            store_row<VEC>(reinterpret_cast<T*>(a.dx) + at, g, ch, D, d[ch]);
-            float s[kE], pg[kE], pb[kE];
-            load_param<VEC>(a.scale, 1.f, g, ch, a.D, s);
-            load_param<VEC>(a.post_gamma, 1.f, g, ch, a.D, pg);
-            load_param<VEC>(a.post_beta, 0.f, g, ch, a.D, pb);
-#pragma unroll
-            for (int i = 0; i < kE; ++i) {
-                if (column<VEC>(g, ch, i) >= D) {   // columns behind the row: no part in any sum
-                    d[ch][i] = 0.f;
-                    b[ch][i] = 0.f;
-                }
-                const float p = fmaf(b[ch][i], pg[i], pb[i]);
-                sums.add(Q_SCALE, ch, i, d[ch][i] * gate[ch][i] * p);
-                const float ds = d[ch][i] * s[i];
-                const float dp = ds * gate[ch][i];
-                if (a.gate_kind == JFA_GATE_IDENTITY) {
-                    u[ch][i] = ds * p;
-                } else if (a.gate_kind != JFA_GATE_NONE) {
-                    const float v = u[ch][i], q = sigmoid(v);
-                    u[ch][i] = ds * p * (a.gate_kind == JFA_GATE_SILU ? q * fmaf(v, 1.0f - q, 1.0f) : q * (1.0f - q));
-                }
-                sums.add(Q_POST_GAMMA, ch, i, dp * b[ch][i]);
-                sums.add(Q_POST_BETA, ch, i, dp);
-                d[ch][i] = dp * pg[i];
-                c1 = fmaf(d[ch][i], b[ch][i], c1);
-                c2 += d[ch][i];
+            rb[ch] = rx[ch] = ru[ch] = rdy[ch] = rdn[ch] = make_uint4(0u, 0u, 0u, 0u);
+            if (live) {
+                rb[ch] = cols.load(a.block, at_next, ch);
+                rx[ch] = cols.load(a.x, at_next, ch);
+                if (gated) ru[ch] = cols.load(a.gate, at_next, ch);
+                if (pre) rdn[ch] = cols.load(a.dn, at_next, ch);
+                rdy[ch] = cols.load(a.dy, at_next, ch);
             }
-            if (a.gate_kind != JFA_GATE_NONE) store_row<VEC>(reinterpret_cast<T*>(a.dgate) + at, g, ch, D, u[ch]);
+        }
+    };
+    if (kAhead) fetch(row < a.rows);
+    float2 w1[P], w0[LN ? P : 1], q1[P];   // s * gamma, s * beta of the block's norm; gamma of the next one's
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const float2 s = make_float2(cols.param(a.scale, 1.f, 2 * i), cols.param(a.scale, 1.f, 2 * i + 1));
+        w1[i] = mul2(s, make_float2(cols.param(a.post_gamma, 1.f, 2 * i), cols.param(a.post_gamma, 1.f, 2 * i + 1)));
+        q1[i] = make_float2(cols.param(a.pre_gamma, 1.f, 2 * i), cols.param(a.pre_gamma, 1.f, 2 * i + 1));
+        if (LN) w0[LN ? i : 0] = mul2(s, make_float2(cols.param(a.post_beta, 0.f, 2 * i), cols.param(a.post_beta, 0.f, 2 * i + 1)));
+    }
+    for (; base < a.rows; base += stride, row += stride, at = at_next) {
+        const bool live = row < a.rows;
+        if (!kAhead) fetch(live);
+        float2 b[P], y[P], u[P], d[P], dn[P], slope[P];
+        cols.get(rb, b);
+        cols.get(rx, y);
+        cols.get(ru, u);
+        cols.get(rdn, dn);
+        cols.get(rdy, d);
+        at_next = at + stride * a.D;
+        if (kAhead) fetch(row + stride < a.rows);
+        float r_b = 1.f;
+        if (a.post != JFA_NORM_NONE) r_b = normalise<T, NCH, LN>(b, a.post, cols, g, inv_d, a.eps);   // b: hat of the block
+        gate_values<P, true>(a.gate_kind, u, slope);                                              // u: act(u)
+        if (pre) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) y[i] = fma2(u[i], LN ? fma2(b[i], w1[i], w0[LN ? i : 0]) : mul2(b[i], w1[i]), y[i]);
+            const float r_y = normalise<T, NCH, LN>(y, a.pre, cols, g, inv_d, a.eps);             // y: hat of y
+            float2 c1 = both(0.f), c2 = both(0.f);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                sums.fma(Q_PRE1, i, dn[i], y[i]);
+                if (LN) sums.add(LN ? Q_PRE0 : 0, i, dn[i]);
+                dn[i] = mul2(dn[i], q1[i]);
+                c1 = fma2(dn[i], y[i], c1);
+                if (LN) c2 = add2(c2, dn[i]);
+            }
+            const float2 c = g.template sum<LN>(c1.x + c1.y, c2.x + c2.y);
+            c1 = both(-c.x * inv_d);
+#pragma unroll
+            for (int i = 0; i < P; ++i) dn[i] = fma2(y[i], c1, dn[i]);
+            if (LN && a.pre == JFA_NORM_LAYER) {
+                c2 = both(-c.y * inv_d);
+#pragma unroll
+                for (int i = 0; i < P; ++i) dn[i] = add2(dn[i], c2);
+                cols.mask(dn);   // no part in the sums below
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) d[i] = fma2(both(r_y), dn[i], d[i]);
+        }
+        // d is dx; on to the block: dp, the gate's gradient and the sums
+        if (live) cols.store(a.dx, at, d);
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                slope[i] = mul2(mul2(d[i], slope[i]), LN ? fma2(b[i], w1[i], w0[LN ? i : 0]) : mul2(b[i], w1[i]));
+            if (live) cols.store(a.dgate, at, slope);
+        }
+        float2 c1 = both(0.f), c2 = both(0.f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            d[i] = mul2(d[i], u[i]);
+            sums.fma(Q_POST1, i, d[i], b[i]);
+            if (LN) sums.add(LN ? Q_POST0 : 0, i, d[i]);
+            d[i] = mul2(d[i], w1[i]);
+            c1 = fma2(d[i], b[i], c1);
+            if (LN) c2 = add2(c2, d[i]);
         }
         if (a.post != JFA_NORM_NONE) {
-            const float2 c = g.sum(c1, c2);
-            c1 = c.x * inv_d;
-            c2 = a.post == JFA_NORM_LAYER ? c.y * inv_d : 0.f;
+            const float2 c = g.template sum<LN>(c1.x + c1.y, c2.x + c2.y);
+            c1 = both(-c.x * inv_d);
+            c2 = both(LN && a.post == JFA_NORM_LAYER ? -c.y * inv_d : 0.f);
 #pragma unroll
-            for (int ch = 0; ch < NCH; ++ch)
-#pragma unroll
-                for (int i = 0; i < kE; ++i) d[ch][i] = rb * (d[ch][i] - fmaf(b[ch][i], c1, c2));
+            for (int i = 0; i < P; ++i) {
+                d[i] = fma2(b[i], c1, d[i]);
+                if (LN) d[i] = add2(d[i], c2);
+                d[i] = mul2(d[i], both(r_b));
+            }
         }
-#pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) store_row<VEC>(reinterpret_cast<T*>(a.dblock) + at, g, ch, D, d[ch]);
+        if (live) cols.store(a.dblock, at, d);
     }
     // this CTA's partial row of each sum
     float* const part = a.parts + (int64_t)blockIdx.x * Q_COUNT * a.D;
+    auto put = [&](float* to, int q) {
+#pragma unroll
+        for (int i = 0; i < 2 * P; ++i) {
+            const float2 v = sums.get(q, i / 2);
+            if (cols.in(i / V, i % V)) to[cols.first(i / V) + i % V] = i & 1 ? v.y : v.x;
+        }
+    };
     if (groups == 1) {
 #pragma unroll
-        for (int q = 0; q < Q_COUNT; ++q)
+        for (int q = 0; q < Q; ++q) put(part + q * a.D, q);
+    } else if (!kSmem) {
+        // the groups' sums in group order, through shared memory [groups][D]
 #pragma unroll
-            for (int ch = 0; ch < NCH; ++ch)
-#pragma unroll
-                for (int i = 0; i < kE; ++i) {
-                    const int c = column<VEC>(g, ch, i);
-                    if (c < a.D) part[q * a.D + c] = sums.get(q, ch, i);
-                }
-    } else if (NCH == 1) {
-        // the groups' sums in group order, through shared memory [groups][G * 8]
-        const int width = G * kE;
-#pragma unroll
-        for (int q = 0; q < Q_COUNT; ++q) {
+        for (int q = 0; q < Q; ++q) {
             __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kE; ++i) smem[(threadIdx.x / G) * width + column<VEC>(g, 0, i)] = sums.get(q, 0, i);
+            put(smem + (threadIdx.x / G) * a.D, q);
             __syncthreads();
             for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
                 float s = 0.f;
-                for (int k = 0; k < groups; ++k) s += smem[k * width + c];
+                for (int k = 0; k < groups; ++k) s += smem[k * a.D + c];
                 part[q * a.D + c] = s;
             }
         }
     }
 }
 
-struct SumOut {
-    float* out[Q_COUNT];
-};
-
-// out[q][c] = sum over the partial rows, in order within eight interleaved
-// strands that are then added in order.
-__global__ void __launch_bounds__(256) block_norm_sum(const float* __restrict__ parts, int n, int D, SumOut o) {
-    __shared__ float s_part[8][33];
-    float* const out = o.out[blockIdx.y];
-    if (!out) return;
+// Adds the partial rows (in order within sixteen interleaved strands, which
+// are then added in order) and forms the parameter gradients: blockIdx.y 0 the
+// block's norm and the scale, 1 the next norm.
+constexpr int kStrands = 16;
+__global__ void __launch_bounds__(32 * kStrands) block_norm_sum(const NormArgs a, int n, float* dscale, float* dpost_gamma,
+                                                                float* dpost_beta, float* dpre_gamma, float* dpre_beta) {
+    __shared__ float2 s_part[kStrands][32];
     const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    float s = 0.f;
-    if (c < D)
-        for (int p = strand; p < n; p += 8) s += parts[((int64_t)p * Q_COUNT + blockIdx.y) * D + c];
+    const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
+    const bool two = (which == 0 ? a.post : a.pre) == JFA_NORM_LAYER;
+    const int64_t pitch = (int64_t)Q_COUNT * a.D;
+    float2 s = make_float2(0.f, 0.f);
+    if (c < a.D) {
+        const float* p1 = a.parts + (int64_t)(which == 0 ? Q_POST1 : Q_PRE1) * a.D + c;
+        const float* p0 = a.parts + (int64_t)(which == 0 ? Q_POST0 : Q_PRE0) * a.D + c;
+#pragma unroll 4
+        for (int p = strand; p < n; p += kStrands) {
+            s.x += p1[p * pitch];
+            if (two) s.y += p0[p * pitch];
+        }
+    }
     s_part[strand][lane] = s;
     __syncthreads();
-    if (strand == 0 && c < D) {
+    if (strand != 0 || c >= a.D) return;
 #pragma unroll
-        for (int k = 1; k < 8; ++k) s += s_part[k][lane];
-        out[c] = s;
+    for (int k = 1; k < kStrands; ++k) {
+        s.x += s_part[k][lane].x;
+        s.y += s_part[k][lane].y;
+    }
+    if (which == 0) {
+        const float sc = a.scale ? a.scale[c] : 1.f;
+        if (dscale) {
+            float v = s.x * (a.post_gamma ? a.post_gamma[c] : 1.f);
+            if (a.post_beta) v = fmaf(s.y, a.post_beta[c], v);
+            dscale[c] = v;
+        }
+        if (dpost_gamma) dpost_gamma[c] = sc * s.x;
+        if (dpost_beta) dpost_beta[c] = sc * s.y;
+    } else {
+        if (dpre_gamma) dpre_gamma[c] = s.x;
+        if (dpre_beta) dpre_beta[c] = s.y;
     }
 }
 
-// Threads per row: one per eight elements, a power of two within a warp,
-// whole warps above.
-int group_size(int D) {
-    const int need = (D + kE - 1) / kE;
-    if (need > 32) return (need + 31) / 32 * 32;
-    int G = 1;
-    while (G < need) G *= 2;
-    return G;
-}
-constexpr int kSmallThreads = 128;   // CTA size for rows within a warp
-
-struct BwdShape {
-    int G, threads, nch, grid;
-    size_t smem;
+// How a row width is cut up: vectors per thread and threads per
+// row, one vector of a row each, a power of two within a warp, whole warps
+// above.  Widths that are no multiple of a vector need one more vector.
+struct RowShape {
+    int G, threads, nch, groups;
+    int period;   // rows after which the alignment repeats
 };
-BwdShape bwd_shape(int64_t rows, int D) {
-    BwdShape s{};
-    s.nch = D > 512 * kE ? 2 : 1;
-    s.G = group_size((D + s.nch - 1) / s.nch);
+// Vectors per thread of the widest rows: 8191 columns that start off a
+// boundary take 1025 vectors of bf16 and 2049 of fp32.
+template <typename T>
+constexpr int kMostChunks = sizeof(T) == 4 ? 5 : 3;
+static_assert(kMostChunks<float> * kMaxThreads * 4 >= kMaxDim + 4 && kMostChunks<__nv_bfloat16> * kMaxThreads * 8 >= kMaxDim + 8,
+              "the widest rows fit");
+
+template <typename T>
+RowShape row_shape(int D) {
+    constexpr int V = Vec<T>::N;
+    RowShape s{};
+    const int vecs = D % V == 0 ? D / V : (D + V - 2) / V + 1;
+    s.nch = vecs <= kMaxThreads ? 1 : (vecs <= 2 * kMaxThreads ? 2 : kMostChunks<T>);
+    const int need = (vecs + s.nch - 1) / s.nch;
+    if (need > 32) {
+        s.G = (need + 31) / 32 * 32;
+    } else {
+        s.G = 1;
+        while (s.G < need) s.G *= 2;
+    }
     s.threads = s.G <= 32 ? kSmallThreads : s.G;
-    const int groups = s.threads / s.G;
+    s.groups = s.threads / s.G;
+    s.period = V;
+    while (s.period > 1 && (int64_t)D * (s.period / 2) % V == 0) s.period /= 2;
+    return s;
+}
+
+// CTAs for `rows` rows: one round if an SM's worth each is enough, else as many
+// as are resident at a time, with the rows of a group gridDim * groups apart,
+// which has to be a multiple of the period.
+template <typename K>
+cudaError_t row_grid(K kern, const RowShape& s, int64_t rows, size_t smem, int64_t limit, int* grid) {
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // about 112 registers a thread: 512 threads fill an SM
-    int64_t cap = (int64_t)sms * (512 / s.threads > 0 ? 512 / s.threads : 1);
-    if (cap > kMaxParts) cap = kMaxParts;
-    const int64_t need = (rows + groups - 1) / groups;
-    s.grid = (int)(need < cap ? need : cap);
-    s.smem = s.nch == 2 ? sizeof(float) * Q_COUNT * 2 * kE * s.G : (groups > 1 ? sizeof(float) * s.threads * kE : 0);
-    return s;
+    const int64_t need = (rows + s.groups - 1) / s.groups;
+    *grid = (int)need;
+    if (need <= sms) return cudaSuccess;
+    int per_sm = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, s.threads, smem);
+    if (e != cudaSuccess) return e;
+    int64_t cap = (int64_t)sms * (per_sm > 0 ? per_sm : 1);
+    if (cap > limit) cap = limit;
+    if (need <= cap) return cudaSuccess;
+    while (cap > 1 && cap * s.groups % s.period != 0) --cap;
+    *grid = (int)cap;
+    return cudaSuccess;
 }
 
 jfa_status check_desc(const jfa_block_norm* d, const char* who) {
@@ -513,30 +620,37 @@ jfa_status check_params(const jfa_block_norm* d, const void* gate, const float* 
     return JFA_OK;
 }
 
-template <typename T>
+template <typename T, bool LN>
 cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
-    const int G = group_size(a.D), threads = G <= 32 ? kSmallThreads : G;
-    const int64_t grid = (a.rows + threads / G - 1) / (threads / G);
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const RowShape s = row_shape<T>(a.D);
+    void (*kern)(NormArgs, int) = s.nch == 1   ? block_norm_fwd<T, 1, LN>
+                                  : s.nch == 2 ? block_norm_fwd<T, 2, LN>
+                                               : block_norm_fwd<T, kMostChunks<T>, LN>;
+    int grid = 0;
+    const cudaError_t e = row_grid(kern, s, a.rows, 0, 0x7fffffff, &grid);
+    if (e != cudaSuccess) return e;
     prof_begin(st);
-    if (a.D % kE == 0) block_norm_fwd<T, true><<<(unsigned)grid, threads, 0, st>>>(a, G);
-    else block_norm_fwd<T, false><<<(unsigned)grid, threads, 0, st>>>(a, G);
+    kern<<<grid, s.threads, 0, st>>>(a, s.G);
     prof_end(st, K_BLOCK_NORM_FWD);
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t bwd_launch(const NormArgs& a, const BwdShape& s, cudaStream_t st) {
-    const bool vec = a.D % kE == 0;
-    void (*kern)(NormArgs, int) =
-        s.nch == 2 ? (vec ? block_norm_bwd<T, true, 2> : block_norm_bwd<T, false, 2>)
-                   : (vec ? block_norm_bwd<T, true, 1> : block_norm_bwd<T, false, 1>);
-    if (s.smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
-        if (e != cudaSuccess) return e;
-    }
+// Returns the number of partial rows in *parts.
+template <typename T, bool LN>
+cudaError_t bwd_launch(const NormArgs& a, int* parts, cudaStream_t st) {
+    const RowShape s = row_shape<T>(a.D);
+    constexpr int Q = LN ? 4 : 2;
+    void (*kern)(NormArgs, int) = s.nch == 1   ? block_norm_bwd<T, 1, LN>
+                                  : s.nch == 2 ? block_norm_bwd<T, 2, LN>
+                                               : block_norm_bwd<T, kMostChunks<T>, LN>;
+    const int E = s.nch * Vec<T>::N;
+    const size_t smem = E > 8 ? sizeof(float) * Q * E * s.G : (s.groups > 1 ? sizeof(float) * s.groups * a.D : 0);
+    cudaError_t e = cudaSuccess;
+    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = row_grid(kern, s, a.rows, smem, kMaxParts, parts);
+    if (e != cudaSuccess) return e;
     prof_begin(st);
-    kern<<<s.grid, s.threads, s.smem, st>>>(a, s.G);
+    kern<<<*parts, s.threads, smem, st>>>(a, s.G);
     prof_end(st, K_BLOCK_NORM_BWD);
     return cudaGetLastError();
 }
@@ -572,7 +686,10 @@ jfa_status jfa_block_norm_forward(const jfa_block_norm* desc, const void* x, con
     a.y = y; a.n = n; a.rows = desc->rows; a.D = desc->dim;
     a.post = desc->post_norm; a.pre = desc->pre_norm; a.gate_kind = desc->gate; a.eps = desc->eps;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = desc->dtype == JFA_F32 ? fwd_launch<float>(a, st) : fwd_launch<__nv_bfloat16>(a, st);
+    const bool ln = desc->post_norm == JFA_NORM_LAYER || desc->pre_norm == JFA_NORM_LAYER;
+    const cudaError_t e = desc->dtype == JFA_F32 ? (ln ? fwd_launch<float, true>(a, st) : fwd_launch<float, false>(a, st))
+                                                 : (ln ? fwd_launch<__nv_bfloat16, true>(a, st)
+                                                       : fwd_launch<__nv_bfloat16, false>(a, st));
     if (e != cudaSuccess) return set_last_error(JFA_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
     return JFA_OK;
 }
@@ -607,13 +724,17 @@ jfa_status jfa_block_norm_backward(const jfa_block_norm* desc, const void* x, co
     a.rows = desc->rows; a.D = desc->dim;
     a.post = desc->post_norm; a.pre = desc->pre_norm; a.gate_kind = desc->gate; a.eps = desc->eps;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const BwdShape shape = bwd_shape(a.rows, a.D);
+    const bool ln = desc->post_norm == JFA_NORM_LAYER || desc->pre_norm == JFA_NORM_LAYER;
+    int parts = 0;
     cudaError_t e = cudaSuccess;
-    if (a.rows > 0) e = desc->dtype == JFA_F32 ? bwd_launch<float>(a, shape, st) : bwd_launch<__nv_bfloat16>(a, shape, st);
+    if (a.rows > 0)
+        e = desc->dtype == JFA_F32 ? (ln ? bwd_launch<float, true>(a, &parts, st) : bwd_launch<float, false>(a, &parts, st))
+                                   : (ln ? bwd_launch<__nv_bfloat16, true>(a, &parts, st)
+                                         : bwd_launch<__nv_bfloat16, false>(a, &parts, st));
     if (e == cudaSuccess && (dscale || dpost_gamma || dpost_beta || dpre_gamma || dpre_beta)) {
-        SumOut o{{dscale, dpost_gamma, dpost_beta, dpre_gamma, dpre_beta}};
         prof_begin(st);
-        block_norm_sum<<<dim3((a.D + 31) / 32, Q_COUNT), 256, 0, st>>>(a.parts, a.rows > 0 ? shape.grid : 0, a.D, o);
+        block_norm_sum<<<dim3((a.D + 31) / 32, 2), 32 * kStrands, 0, st>>>(a, parts, dscale, dpost_gamma, dpost_beta,
+                                                                           dpre_gamma, dpre_beta);
         prof_end(st, K_BLOCK_NORM_SUM);
         e = cudaGetLastError();
     }

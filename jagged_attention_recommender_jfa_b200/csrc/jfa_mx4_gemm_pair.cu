@@ -117,7 +117,27 @@ __device__ __forceinline__ void store_box(const Mx4Params& P, const uint32_t* r,
 }
 
 // Any row start, and bf16 sums: 32 columns through the staging tile, lane =
-// column, a row at a time.
+// column, eight rows under way at a time.
+template <typename T, bool ADD>
+__device__ __forceinline__ void store_rows(const Mx4Params& P, const float* stage, int row0, int col0, int lane, int rows,
+                                           int cols, float b) {
+    constexpr int kAhead = 8;
+    const bool in = lane < cols;
+    T* o = reinterpret_cast<T*>(P.out) + (int64_t)row0 * P.n + col0 + (in ? lane : 0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < rows; i0 += kAhead, o += (int64_t)kAhead * P.n) {
+        float v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            v[i] = stage[(i0 + i) * 32 + (lane ^ (i0 + i))] + b;
+            if (ADD && i0 + i < rows) v[i] += to_f(o[(int64_t)i * P.n]);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (in && i0 + i < rows) o[(int64_t)i * P.n] = from_f<T>(v[i]);
+    }
+}
+
 __device__ __forceinline__ void store_any(const Mx4Params& P, const uint32_t* r, int row0, int col0, int lane,
                                           float* stage) {
     const int rows = min(32, P.m - row0), cols = min(32, P.n - col0);
@@ -126,20 +146,13 @@ __device__ __forceinline__ void store_any(const Mx4Params& P, const uint32_t* r,
 #pragma unroll
     for (int t = 0; t < 32; ++t) stage[lane * 32 + (t ^ lane)] = __uint_as_float(r[t]);
     __syncwarp();
-    const bool in = lane < cols;
-    const float b = (P.bias && in) ? __ldg(P.bias + col0 + lane) : 0.f;
-    int64_t at = (int64_t)row0 * P.n + col0 + lane;
-#pragma unroll 4
-    for (int i = 0; i < rows; ++i, at += P.n) {
-        float v = stage[i * 32 + (lane ^ i)] + b;
-        if (!in) continue;
-        if (P.out_bf16) {
-            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(P.out) + at;
-            *o = __float2bfloat16_rn(P.accumulate ? v + __bfloat162float(*o) : v);
-        } else {
-            float* o = reinterpret_cast<float*>(P.out) + at;
-            *o = P.accumulate ? v + *o : v;
-        }
+    const float b = (P.bias && lane < cols) ? __ldg(P.bias + col0 + lane) : 0.f;
+    if (P.out_bf16) {
+        if (P.accumulate) store_rows<__nv_bfloat16, true>(P, stage, row0, col0, lane, rows, cols, b);
+        else store_rows<__nv_bfloat16, false>(P, stage, row0, col0, lane, rows, cols, b);
+    } else {
+        if (P.accumulate) store_rows<float, true>(P, stage, row0, col0, lane, rows, cols, b);
+        else store_rows<float, false>(P, stage, row0, col0, lane, rows, cols, b);
     }
     __syncwarp();
 }

@@ -62,36 +62,55 @@ struct NormArgs {
 
 // Group of threads that shares a row: G lanes of a warp (several rows per
 // warp) or whole warps, then one row per CTA.
+struct GroupBuf {
+    float4 a[2][kMaxThreads / 128], b[2][kMaxThreads / 128];   // a sum of each warp, two turns
+};
 struct Group {
     int G, t;          // size, index in the group
     int warps;         // 1: within a warp
-    float2* buf;       // [2][32]
+    GroupBuf* buf;
     int turn;
-    __device__ __forceinline__ Group(int G_, float2* b) : G(G_), t(threadIdx.x % G_), warps(G_ <= 32 ? 1 : G_ / 32), buf(b), turn(0) {}
+    __device__ __forceinline__ Group(int G_, GroupBuf* b) : G(G_), t(threadIdx.x % G_), warps(G_ <= 32 ? 1 : G_ / 32), buf(b), turn(0) {
+        if (warps == 1) return;
+        // entries of warps that do not exist stay zero
+        for (int i = threadIdx.x; i < (int)(sizeof(GroupBuf) / 4); i += blockDim.x) reinterpret_cast<float*>(buf)[i] = 0.f;
+        __syncthreads();
+    }
+    __device__ __forceinline__ float total(const float4* p) const {
+        float4 s = p[0];
+#pragma unroll
+        for (int i = 1; i < kMaxThreads / 128; ++i)
+            if (warps > 4 * i) {
+                const float4 q = p[i];
+                s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
+            }
+        return (s.x + s.y) + (s.z + s.w);
+    }
     // sums of a (and b) over the group, in every thread
     template <bool TWO>
     __device__ __forceinline__ float2 sum(float a, float b) {
-        const int width = G < 32 ? G : 32;
+        if (G >= 32) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            if (o < width) {
+            for (int o = 16; o > 0; o >>= 1) {
                 a += __shfl_xor_sync(0xffffffffu, a, o);
                 if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
             }
+            if (warps == 1) return make_float2(a, b);
+            // alternating buffers: one barrier per sum
+            const int k = turn & 1, w = threadIdx.x >> 5;
+            ++turn;
+            if ((threadIdx.x & 31) == 0) {
+                reinterpret_cast<float*>(buf->a[k])[w] = a;
+                if (TWO) reinterpret_cast<float*>(buf->b[k])[w] = b;
+            }
+            __syncthreads();
+            return make_float2(total(buf->a[k]), TWO ? total(buf->b[k]) : 0.f);
         }
-        if (warps == 1) return make_float2(a, b);
-        // alternating buffers: one barrier per sum
-        float2* const p = buf + (turn & 1) * 32;
-        ++turn;
-        if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        float2 s = p[0];
-        for (int w = 1; w < warps; ++w) {
-            const float2 q = p[w];
-            s.x += q.x;
-            if (TWO) s.y += q.y;
+        for (int o = G >> 1; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
         }
-        return s;
+        return make_float2(a, b);
     }
 };
 
@@ -149,18 +168,32 @@ struct Cols {
     __device__ __forceinline__ bool full(int ch) const { return first(ch) >= 0 && first(ch) + V <= D; }
     __device__ __forceinline__ bool in(int ch, int u) const { return (unsigned)(first(ch) + u) < (unsigned)D; }
 
-    // `at`: offset of the row's column 0
-    __device__ __forceinline__ uint4 load(const void* base, int64_t at, int ch) const {
-        if (!any(ch)) return make_uint4(0u, 0u, 0u, 0u);
-        const T* p = reinterpret_cast<const T*>(base) + (at + first(ch));
-        if (at + first(ch) + V <= total) return __ldg(reinterpret_cast<const uint4*>(p));
-        // the tensor ends inside this vector
-        uint4 r = make_uint4(0u, 0u, 0u, 0u);
-        T* e = reinterpret_cast<T*>(&r);
+    // the thread's vectors of N tensors (absent ones NULL: zero) for the row
+    // whose column 0 is at offset `at`
+    template <int N>
+    __device__ __forceinline__ void load(const void* const (&base)[N], int64_t at, bool live, uint4 (&r)[N][NCH]) const {
 #pragma unroll
-        for (int u = 0; u < V; ++u)
-            if (in(ch, u)) e[u] = p[u];
-        return r;
+        for (int ch = 0; ch < NCH; ++ch) {
+            const int64_t off = at + first(ch);
+            const bool here = live && any(ch);
+            if (!here || off + V > total) {
+#pragma unroll
+                for (int n = 0; n < N; ++n) r[n][ch] = make_uint4(0u, 0u, 0u, 0u);
+                if (!here) continue;
+                // the tensor ends inside this vector
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    if (base[n])
+#pragma unroll
+                        for (int u = 0; u < V; ++u)
+                            if (in(ch, u)) reinterpret_cast<T*>(&r[n][ch])[u] = reinterpret_cast<const T*>(base[n])[off + u];
+                continue;
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                r[n][ch] = base[n] ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(base[n]) + off))
+                                   : make_uint4(0u, 0u, 0u, 0u);
+        }
     }
     // elements outside the row (a neighbour's, or nothing) to zero
     __device__ __forceinline__ void mask(float2 (&f)[P]) const {
@@ -194,6 +227,38 @@ struct Cols {
         const int ch = i / V, u = i % V;
         return in(ch, u) ? (p ? __ldg(p + first(ch) + u) : absent) : 0.f;
     }
+};
+
+// A thread's parameters, K vectors of P pairs.  With one vector per thread and
+// tensor (MEM) they wait in shared memory, each thread its own: registers are
+// what limits the warps of an SM there, and those hide the latencies of the
+// row sums.  Wider rows keep them in registers.
+template <int K, int P, bool MEM>
+struct Params {
+    float2 v[K][P];
+    __device__ __forceinline__ Params(float*) {}
+    __device__ __forceinline__ void set(int k, int i, float2 x) { v[k][i] = x; }
+    __device__ __forceinline__ void get(int k, float2 (&f)[P]) const {
+#pragma unroll
+        for (int i = 0; i < P; ++i) f[i] = v[k][i];
+    }
+};
+template <int K, int P>
+struct Params<K, P, true> {
+    float4* mine;
+    __device__ __forceinline__ Params(float* smem) : mine(reinterpret_cast<float4*>(smem) + threadIdx.x) {}
+    __device__ __forceinline__ void set(int k, int i, float2 x) {
+        reinterpret_cast<float2*>(mine + (k * (P / 2) + i / 2) * blockDim.x)[i & 1] = x;
+    }
+    __device__ __forceinline__ void get(int k, float2 (&f)[P]) const {
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            const float4 q = mine[(k * (P / 2) + i / 2) * blockDim.x];
+            f[i] = make_float2(q.x, q.y);
+            f[i + 1] = make_float2(q.z, q.w);
+        }
+    }
+    static constexpr size_t bytes(int threads) { return sizeof(float2) * K * P * threads; }
 };
 
 // 1 / (1 + e^-u) with the hardware's base-2 exponential and reciprocal (a few
@@ -256,64 +321,67 @@ __device__ __forceinline__ float normalise(float2 (&v)[Cols<T, NCH>::P], int kin
     return r;
 }
 
+// v * (vector k1) (+ vector k0) in place.
+template <int P, bool LN, typename Par>
+__device__ __forceinline__ void scale_shift(const Par& par, int k1, int k0, float2 (&v)[P]) {
+    float2 w[P];
+    par.get(k1, w);
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = mul2(v[i], w[i]);
+    if (LN) {
+        par.get(k0, w);
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = add2(v[i], w[i]);
+    }
+}
+
 // LN: a norm is a LayerNorm, so that there may be betas.
 template <typename T, int NCH, bool LN>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd(const NormArgs a, int G) {
     constexpr int P = Cols<T, NCH>::P;
-    __shared__ float2 buf[64];
-    Group g(G, buf);
+    extern __shared__ float4 smem4[];
+    __shared__ GroupBuf buf;
+    Group g(G, &buf);
+    Params<LN ? 4 : 2, P, NCH == 1> par(reinterpret_cast<float*>(smem4));
     const int groups = blockDim.x / G;
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t base = (int64_t)blockIdx.x * groups, row = base + threadIdx.x / G;
     const Cols<T, NCH> cols(a.D, a.rows, row, g);
     const bool gated = a.gate_kind != JFA_GATE_NONE, pre = a.pre != JFA_NORM_NONE;
     const float inv_d = 1.0f / (float)a.D;
-    uint4 rb[NCH], rx[NCH], ru[NCH];
+    const void* const in[3] = {a.block, a.x, gated ? a.gate : nullptr};
+    uint4 raw[3][NCH];
     int64_t at = row * a.D, at_next = at;
-    auto fetch = [&](bool live) {
-#pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-            rb[ch] = rx[ch] = ru[ch] = make_uint4(0u, 0u, 0u, 0u);
-            if (live) {
-                rb[ch] = cols.load(a.block, at_next, ch);
-                rx[ch] = cols.load(a.x, at_next, ch);
-                if (gated) ru[ch] = cols.load(a.gate, at_next, ch);
-            }
-        }
-    };
-    fetch(row < a.rows);
+    cols.load(in, at, row < a.rows, raw);
     // y = x + act(u) * (w1 * hat + w0), n = hat_y * q1 + q0
-    float2 w1[P], w0[LN ? P : 1], q1[P], q0[LN ? P : 1];
+    enum { W1 = 0, Q1, W0, Q0 };
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const float2 s = make_float2(cols.param(a.scale, 1.f, 2 * i), cols.param(a.scale, 1.f, 2 * i + 1));
-        w1[i] = mul2(s, make_float2(cols.param(a.post_gamma, 1.f, 2 * i), cols.param(a.post_gamma, 1.f, 2 * i + 1)));
-        q1[i] = make_float2(cols.param(a.pre_gamma, 1.f, 2 * i), cols.param(a.pre_gamma, 1.f, 2 * i + 1));
+        par.set(W1, i, mul2(s, make_float2(cols.param(a.post_gamma, 1.f, 2 * i), cols.param(a.post_gamma, 1.f, 2 * i + 1))));
+        par.set(Q1, i, make_float2(cols.param(a.pre_gamma, 1.f, 2 * i), cols.param(a.pre_gamma, 1.f, 2 * i + 1)));
         if (LN) {
-            w0[LN ? i : 0] = mul2(s, make_float2(cols.param(a.post_beta, 0.f, 2 * i), cols.param(a.post_beta, 0.f, 2 * i + 1)));
-            q0[LN ? i : 0] = make_float2(cols.param(a.pre_beta, 0.f, 2 * i), cols.param(a.pre_beta, 0.f, 2 * i + 1));
+            par.set(LN ? W0 : 0, i, mul2(s, make_float2(cols.param(a.post_beta, 0.f, 2 * i), cols.param(a.post_beta, 0.f, 2 * i + 1))));
+            par.set(LN ? Q0 : 0, i, make_float2(cols.param(a.pre_beta, 0.f, 2 * i), cols.param(a.pre_beta, 0.f, 2 * i + 1)));
         }
     }
     for (; base < a.rows; base += stride, row += stride, at = at_next) {
         float2 b[P], x[P], k[P], none[1];
-        cols.get(rb, b);
-        cols.get(rx, x);
-        cols.get(ru, k);
+        cols.get(raw[0], b);
+        cols.get(raw[1], x);
+        cols.get(raw[2], k);
         at_next = at + stride * a.D;
-        fetch(row + stride < a.rows);
+        cols.load(in, at_next, row + stride < a.rows, raw);
         if (a.post != JFA_NORM_NONE) normalise<T, NCH, LN>(b, a.post, cols, g, inv_d, a.eps);
         if (gated) gate_values<P, false>(a.gate_kind, k, none);
+        scale_shift<P, LN>(par, W1, LN ? W0 : 0, b);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float2 p = LN ? fma2(b[i], w1[i], w0[LN ? i : 0]) : mul2(b[i], w1[i]);
-            x[i] = gated ? fma2(k[i], p, x[i]) : add2(x[i], p);
-        }
+        for (int i = 0; i < P; ++i) x[i] = gated ? fma2(k[i], b[i], x[i]) : add2(x[i], b[i]);
         const bool live = row < a.rows;
         if (live) cols.store(a.y, at, x);
         if (!pre) continue;
         normalise<T, NCH, LN>(x, a.pre, cols, g, inv_d, a.eps);
-#pragma unroll
-        for (int i = 0; i < P; ++i) x[i] = LN ? fma2(x[i], q1[i], q0[LN ? i : 0]) : mul2(x[i], q1[i]);
+        scale_shift<P, LN>(par, Q1, LN ? Q0 : 0, x);
         if (live) cols.store(a.n, at, x);
     }
 }
@@ -354,12 +422,14 @@ struct Sums<P, Q, true> {
 };
 
 template <typename T, int NCH, bool LN>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_bwd(const NormArgs a, int G) {
+__global__ void __launch_bounds__(sizeof(T) == 4 && NCH == 1 ? 640 : kMaxThreads) block_norm_bwd(const NormArgs a, int G) {
     constexpr int V = Vec<T>::N, P = Cols<T, NCH>::P, Q = LN ? 4 : 2;
     constexpr bool kSmem = P > 4, kAhead = NCH == 1;
-    extern __shared__ float smem[];   // P > 4: the sums; small groups: the CTA's reduction
-    __shared__ float2 buf[64];
-    Group g(G, buf);
+    extern __shared__ float4 smem4[];   // one vector: parameters, then the reduction of small groups; else the sums
+    float* const smem = reinterpret_cast<float*>(smem4);
+    __shared__ GroupBuf buf;
+    Group g(G, &buf);
+    Params<LN ? 3 : 2, P, NCH == 1> par(smem);
     Sums<P, Q, kSmem> sums(smem, g);
     const int groups = blockDim.x / G;
     const int64_t stride = (int64_t)gridDim.x * groups;
@@ -367,54 +437,48 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd(const NormArgs a, 
     const Cols<T, NCH> cols(a.D, a.rows, row, g);
     const bool gated = a.gate_kind != JFA_GATE_NONE, pre = a.pre != JFA_NORM_NONE;
     const float inv_d = 1.0f / (float)a.D;
-    uint4 rb[NCH], rx[NCH], ru[NCH], rdy[NCH], rdn[NCH];
+    const void* const in[5] = {a.block, a.x, gated ? a.gate : nullptr, pre ? a.dn : nullptr, a.dy};
+    uint4 raw[5][NCH];
     int64_t at = row * a.D, at_next = at;
-    auto fetch = [&](bool live) {
-#pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-            rb[ch] = rx[ch] = ru[ch] = rdy[ch] = rdn[ch] = make_uint4(0u, 0u, 0u, 0u);
-            if (live) {
-                rb[ch] = cols.load(a.block, at_next, ch);
-                rx[ch] = cols.load(a.x, at_next, ch);
-                if (gated) ru[ch] = cols.load(a.gate, at_next, ch);
-                if (pre) rdn[ch] = cols.load(a.dn, at_next, ch);
-                rdy[ch] = cols.load(a.dy, at_next, ch);
-            }
-        }
-    };
-    if (kAhead) fetch(row < a.rows);
-    float2 w1[P], w0[LN ? P : 1], q1[P];   // s * gamma, s * beta of the block's norm; gamma of the next one's
+    if (kAhead) cols.load(in, at, row < a.rows, raw);
+    enum { W1 = 0, Q1, W0 };   // s * gamma of the block's norm, gamma of the next one's, s * beta
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const float2 s = make_float2(cols.param(a.scale, 1.f, 2 * i), cols.param(a.scale, 1.f, 2 * i + 1));
-        w1[i] = mul2(s, make_float2(cols.param(a.post_gamma, 1.f, 2 * i), cols.param(a.post_gamma, 1.f, 2 * i + 1)));
-        q1[i] = make_float2(cols.param(a.pre_gamma, 1.f, 2 * i), cols.param(a.pre_gamma, 1.f, 2 * i + 1));
-        if (LN) w0[LN ? i : 0] = mul2(s, make_float2(cols.param(a.post_beta, 0.f, 2 * i), cols.param(a.post_beta, 0.f, 2 * i + 1)));
+        par.set(W1, i, mul2(s, make_float2(cols.param(a.post_gamma, 1.f, 2 * i), cols.param(a.post_gamma, 1.f, 2 * i + 1))));
+        par.set(Q1, i, make_float2(cols.param(a.pre_gamma, 1.f, 2 * i), cols.param(a.pre_gamma, 1.f, 2 * i + 1)));
+        if (LN)
+            par.set(LN ? W0 : 0, i, mul2(s, make_float2(cols.param(a.post_beta, 0.f, 2 * i), cols.param(a.post_beta, 0.f, 2 * i + 1))));
     }
     for (; base < a.rows; base += stride, row += stride, at = at_next) {
         const bool live = row < a.rows;
-        if (!kAhead) fetch(live);
+        if (!kAhead) cols.load(in, at, live, raw);
         float2 b[P], y[P], u[P], d[P], dn[P], slope[P];
-        cols.get(rb, b);
-        cols.get(rx, y);
-        cols.get(ru, u);
-        cols.get(rdn, dn);
-        cols.get(rdy, d);
+        cols.get(raw[0], b);
+        cols.get(raw[1], y);
+        cols.get(raw[2], u);
+        cols.get(raw[3], dn);
+        cols.get(raw[4], d);
         at_next = at + stride * a.D;
-        if (kAhead) fetch(row + stride < a.rows);
+        if (kAhead) cols.load(in, at_next, row + stride < a.rows, raw);
         float r_b = 1.f;
         if (a.post != JFA_NORM_NONE) r_b = normalise<T, NCH, LN>(b, a.post, cols, g, inv_d, a.eps);   // b: hat of the block
         gate_values<P, true>(a.gate_kind, u, slope);                                              // u: act(u)
         if (pre) {
+            float2 w[P];
 #pragma unroll
-            for (int i = 0; i < P; ++i) y[i] = fma2(u[i], LN ? fma2(b[i], w1[i], w0[LN ? i : 0]) : mul2(b[i], w1[i]), y[i]);
+            for (int i = 0; i < P; ++i) w[i] = b[i];
+            scale_shift<P, LN>(par, W1, LN ? W0 : 0, w);
+#pragma unroll
+            for (int i = 0; i < P; ++i) y[i] = fma2(u[i], w[i], y[i]);
             const float r_y = normalise<T, NCH, LN>(y, a.pre, cols, g, inv_d, a.eps);             // y: hat of y
             float2 c1 = both(0.f), c2 = both(0.f);
+            par.get(Q1, w);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 sums.fma(Q_PRE1, i, dn[i], y[i]);
                 if (LN) sums.add(LN ? Q_PRE0 : 0, i, dn[i]);
-                dn[i] = mul2(dn[i], q1[i]);
+                dn[i] = mul2(dn[i], w[i]);
                 c1 = fma2(dn[i], y[i], c1);
                 if (LN) c2 = add2(c2, dn[i]);
             }
@@ -433,19 +497,23 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd(const NormArgs a, 
         }
         // d is dx; on to the block: dp, the gate's gradient and the sums
         if (live) cols.store(a.dx, at, d);
+        float2 w[P];
         if (gated) {
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                slope[i] = mul2(mul2(d[i], slope[i]), LN ? fma2(b[i], w1[i], w0[LN ? i : 0]) : mul2(b[i], w1[i]));
+            for (int i = 0; i < P; ++i) w[i] = b[i];
+            scale_shift<P, LN>(par, W1, LN ? W0 : 0, w);
+#pragma unroll
+            for (int i = 0; i < P; ++i) slope[i] = mul2(mul2(d[i], slope[i]), w[i]);
             if (live) cols.store(a.dgate, at, slope);
         }
         float2 c1 = both(0.f), c2 = both(0.f);
+        par.get(W1, w);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             d[i] = mul2(d[i], u[i]);
             sums.fma(Q_POST1, i, d[i], b[i]);
             if (LN) sums.add(LN ? Q_POST0 : 0, i, d[i]);
-            d[i] = mul2(d[i], w1[i]);
+            d[i] = mul2(d[i], w[i]);
             c1 = fma2(d[i], b[i], c1);
             if (LN) c2 = add2(c2, d[i]);
         }
@@ -476,6 +544,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd(const NormArgs a, 
         for (int q = 0; q < Q; ++q) put(part + q * a.D, q);
     } else if (!kSmem) {
         // the groups' sums in group order, through shared memory [groups][D]
+        // (behind the last use of the parameters)
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             __syncthreads();
@@ -620,17 +689,25 @@ jfa_status check_params(const jfa_block_norm* d, const void* gate, const float* 
     return JFA_OK;
 }
 
+template <typename K>
+cudaError_t allow_smem(K kern, size_t smem) {
+    // 48 KB, static shared memory included, need no permission
+    return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
+}
+
 template <typename T, bool LN>
 cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
     const RowShape s = row_shape<T>(a.D);
     void (*kern)(NormArgs, int) = s.nch == 1   ? block_norm_fwd<T, 1, LN>
                                   : s.nch == 2 ? block_norm_fwd<T, 2, LN>
                                                : block_norm_fwd<T, kMostChunks<T>, LN>;
+    const size_t smem = s.nch == 1 ? Params<LN ? 4 : 2, Vec<T>::N / 2, true>::bytes(s.threads) : 0;
     int grid = 0;
-    const cudaError_t e = row_grid(kern, s, a.rows, 0, 0x7fffffff, &grid);
+    cudaError_t e = allow_smem(kern, smem);
+    if (e == cudaSuccess) e = row_grid(kern, s, a.rows, smem, 0x7fffffff, &grid);
     if (e != cudaSuccess) return e;
     prof_begin(st);
-    kern<<<grid, s.threads, 0, st>>>(a, s.G);
+    kern<<<grid, s.threads, smem, st>>>(a, s.G);
     prof_end(st, K_BLOCK_NORM_FWD);
     return cudaGetLastError();
 }
@@ -643,10 +720,11 @@ cudaError_t bwd_launch(const NormArgs& a, int* parts, cudaStream_t st) {
     void (*kern)(NormArgs, int) = s.nch == 1   ? block_norm_bwd<T, 1, LN>
                                   : s.nch == 2 ? block_norm_bwd<T, 2, LN>
                                                : block_norm_bwd<T, kMostChunks<T>, LN>;
-    const int E = s.nch * Vec<T>::N;
-    const size_t smem = E > 8 ? sizeof(float) * Q * E * s.G : (s.groups > 1 ? sizeof(float) * s.groups * a.D : 0);
-    cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const int pairs = s.nch * Vec<T>::N / 2;
+    size_t smem = pairs > 4 ? sizeof(float2) * Q * pairs * s.G : 0;   // the sums
+    if (s.nch == 1) smem = Params<LN ? 3 : 2, Vec<T>::N / 2, true>::bytes(s.threads);
+    if (s.groups > 1 && smem < sizeof(float) * s.groups * a.D) smem = sizeof(float) * s.groups * a.D;
+    cudaError_t e = allow_smem(kern, smem);
     if (e == cudaSuccess) e = row_grid(kern, s, a.rows, smem, kMaxParts, parts);
     if (e != cudaSuccess) return e;
     prof_begin(st);

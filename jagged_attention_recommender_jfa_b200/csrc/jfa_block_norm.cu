@@ -62,8 +62,9 @@ struct NormArgs {
 
 // Group of threads that shares a row: G lanes of a warp (several rows per
 // warp) or whole warps, then one row per CTA.
+constexpr int kMostSums = 3;
 struct GroupBuf {
-    float4 a[2][kMaxThreads / 128], b[2][kMaxThreads / 128];   // a sum of each warp, two turns
+    float4 v[2][kMostSums][kMaxThreads / 128];   // [turn][which sum], a float per warp
 };
 struct Group {
     int G, t;          // size, index in the group
@@ -86,31 +87,30 @@ struct Group {
             }
         return (s.x + s.y) + (s.z + s.w);
     }
-    // sums of a (and b) over the group, in every thread
-    template <bool TWO>
-    __device__ __forceinline__ float2 sum(float a, float b) {
+    // sums of N values over the group, in every thread
+    template <int N>
+    __device__ __forceinline__ void sum(float (&v)[N]) {
+        static_assert(N <= kMostSums, "buffer");
         if (G >= 32) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                a += __shfl_xor_sync(0xffffffffu, a, o);
-                if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
-            }
-            if (warps == 1) return make_float2(a, b);
-            // alternating buffers: one barrier per sum
-            const int k = turn & 1, w = threadIdx.x >> 5;
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+            if (warps == 1) return;
+            // alternating buffers: one barrier per turn
+            const int k = turn & 1;
             ++turn;
-            if ((threadIdx.x & 31) == 0) {
-                reinterpret_cast<float*>(buf->a[k])[w] = a;
-                if (TWO) reinterpret_cast<float*>(buf->b[k])[w] = b;
-            }
+            if ((threadIdx.x & 31) == 0)
+#pragma unroll
+                for (int n = 0; n < N; ++n) reinterpret_cast<float*>(buf->v[k][n])[threadIdx.x >> 5] = v[n];
             __syncthreads();
-            return make_float2(total(buf->a[k]), TWO ? total(buf->b[k]) : 0.f);
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] = total(buf->v[k][n]);
+            return;
         }
-        for (int o = G >> 1; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
-        return make_float2(a, b);
+        for (int o = G >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
     }
 };
 
@@ -298,27 +298,29 @@ __device__ __forceinline__ void gate_values(int kind, float2 (&u)[P], float2 (&s
     }
 }
 
-// Turns v into (v - mu) * r in place (0 outside the row) and returns r.
-template <typename T, int NCH, bool LN>
-__device__ __forceinline__ float normalise(float2 (&v)[Cols<T, NCH>::P], int kind, const Cols<T, NCH>& cols, Group& g,
-                                           float inv_d, float eps) {
-    constexpr int P = Cols<T, NCH>::P;
-    if (LN && kind == JFA_NORM_LAYER) {
-        float2 s = v[0];
+template <int P>
+__device__ __forceinline__ float dot(const float2 (&a)[P], const float2 (&b)[P]) {
+    float2 q = mul2(a[0], b[0]);
 #pragma unroll
-        for (int i = 1; i < P; ++i) s = add2(s, v[i]);
-        const float mu = g.template sum<false>(s.x + s.y, 0.f).x / (float)cols.D;   // exact for a constant row of exact sum
+    for (int i = 1; i < P; ++i) q = fma2(a[i], b[i], q);
+    return q.x + q.y;
+}
+template <int P>
+__device__ __forceinline__ float plain_sum(const float2 (&a)[P]) {
+    float2 q = a[0];
 #pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = add2(v[i], both(-mu));
-        cols.mask(v);
-    }
-    float2 q = mul2(v[0], v[0]);
+    for (int i = 1; i < P; ++i) q = add2(q, a[i]);
+    return q.x + q.y;
+}
+template <int P>
+__device__ __forceinline__ void scale_by(float2 (&a)[P], float r) {
 #pragma unroll
-    for (int i = 1; i < P; ++i) q = fma2(v[i], v[i], q);
-    const float r = rsqrtf(fmaf(g.template sum<false>(q.x + q.y, 0.f).x, inv_d, eps));
+    for (int i = 0; i < P; ++i) a[i] = mul2(a[i], both(r));
+}
+template <int P>
+__device__ __forceinline__ void shift_by(float2 (&a)[P], float r) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = mul2(v[i], both(r));
-    return r;
+    for (int i = 0; i < P; ++i) a[i] = add2(a[i], both(r));
 }
 
 // v * (vector k1) (+ vector k0) in place.
@@ -335,9 +337,63 @@ __device__ __forceinline__ void scale_shift(const Par& par, int k1, int k0, floa
     }
 }
 
+// The block's norm and the way to y.  In: b, x, k = act(u) (ones without a
+// gate).  Out: b = hat of the block, x = y - mu_y with mu_y the mean for a
+// LayerNorm next and 0 otherwise; returns the block's r.  The mean of
+//   y = x + k (w0 + w1 hat) = (x + k w0) + r (k w1 c),  c = b - mu
+// comes from two sums taken together with the sum of c^2, so that it needs no
+// turn of its own; y is the sum of its parts either way.
+template <typename T, int NCH, bool LN, typename Par>
+__device__ __forceinline__ float to_y(const Par& par, int W1, int W0, int post, int pre, const Cols<T, NCH>& cols, Group& g,
+                                      float inv_d, float eps, float2 (&b)[Cols<T, NCH>::P], float2 (&x)[Cols<T, NCH>::P],
+                                      const float2 (&k)[Cols<T, NCH>::P], float& mu_y) {
+    constexpr int P = Cols<T, NCH>::P;
+    if (LN && post == JFA_NORM_LAYER) {
+        float s[1] = {plain_sum<P>(b)};
+        g.template sum<1>(s);
+        shift_by<P>(b, -s[0] / (float)cols.D);   // exact for a constant row of exact sum
+        cols.mask(b);
+    }
+    float2 w[P];
+    if (LN) {
+        par.get(W0, w);
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = fma2(k[i], w[i], x[i]);
+    }
+    par.get(W1, w);
+#pragma unroll
+    for (int i = 0; i < P; ++i) w[i] = mul2(mul2(w[i], k[i]), b[i]);
+    float r = 1.f;
+    mu_y = 0.f;
+    if (LN && pre == JFA_NORM_LAYER) {
+        float s[3] = {dot<P>(b, b), plain_sum<P>(x), plain_sum<P>(w)};
+        g.template sum<3>(s);
+        if (post != JFA_NORM_NONE) r = rsqrtf(fmaf(s[0], inv_d, eps));
+        mu_y = fmaf(r, s[2], s[1]) * inv_d;
+    } else if (post != JFA_NORM_NONE) {
+        float s[1] = {dot<P>(b, b)};
+        g.template sum<1>(s);
+        r = rsqrtf(fmaf(s[0], inv_d, eps));
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = fma2(both(r), w[i], x[i]);
+    if (post != JFA_NORM_NONE) scale_by<P>(b, r);
+    return r;
+}
+
+// Registers per thread through the launch bound: 80 for the forward (64 fp32)
+// and 80 for the fp32 backward with one vector per thread, 128 otherwise.
+// 60000 x 1024 fp32 backward at 128 / 96 / 80 / 64 registers: 451 / 383 / 331 /
+// 350 us; 222283 x 1024 bf16 backward at 128 / 96 / 80: 769 / 1228 / 1670 us
+// (spills), forward at 80 / 64: 393 / 431 us.
+template <typename T, int NCH>
+constexpr int kFwdBound = NCH > 1 ? kMaxThreads : (sizeof(T) == 4 ? 1024 : 768);
+template <typename T, int NCH>
+constexpr int kBwdBound = NCH == 1 && sizeof(T) == 4 ? 768 : kMaxThreads;
+
 // LN: a norm is a LayerNorm, so that there may be betas.
 template <typename T, int NCH, bool LN>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_fwd(const NormArgs a, int G) {
+__global__ void __launch_bounds__(kFwdBound<T, NCH>) block_norm_fwd(const NormArgs a, int G) {
     constexpr int P = Cols<T, NCH>::P;
     extern __shared__ float4 smem4[];
     __shared__ GroupBuf buf;
@@ -372,15 +428,19 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd(const NormArgs a, 
         cols.get(raw[2], k);
         at_next = at + stride * a.D;
         cols.load(in, at_next, row + stride < a.rows, raw);
-        if (a.post != JFA_NORM_NONE) normalise<T, NCH, LN>(b, a.post, cols, g, inv_d, a.eps);
-        if (gated) gate_values<P, false>(a.gate_kind, k, none);
-        scale_shift<P, LN>(par, W1, LN ? W0 : 0, b);
-#pragma unroll
-        for (int i = 0; i < P; ++i) x[i] = gated ? fma2(k[i], b[i], x[i]) : add2(x[i], b[i]);
+        gate_values<P, false>(a.gate_kind, k, none);
+        float mu;
+        to_y<T, NCH, LN>(par, W1, LN ? W0 : 0, a.post, a.pre, cols, g, inv_d, a.eps, b, x, k, mu);
         const bool live = row < a.rows;
         if (live) cols.store(a.y, at, x);
         if (!pre) continue;
-        normalise<T, NCH, LN>(x, a.pre, cols, g, inv_d, a.eps);
+        if (LN && a.pre == JFA_NORM_LAYER) {
+            shift_by<P>(x, -mu);
+            cols.mask(x);
+        }
+        float s[1] = {dot<P>(x, x)};
+        g.template sum<1>(s);
+        scale_by<P>(x, rsqrtf(fmaf(s[0], inv_d, a.eps)));
         scale_shift<P, LN>(par, Q1, LN ? Q0 : 0, x);
         if (live) cols.store(a.n, at, x);
     }
@@ -422,7 +482,7 @@ struct Sums<P, Q, true> {
 };
 
 template <typename T, int NCH, bool LN>
-__global__ void __launch_bounds__(sizeof(T) == 4 && NCH == 1 ? 640 : kMaxThreads) block_norm_bwd(const NormArgs a, int G) {
+__global__ void __launch_bounds__(kBwdBound<T, NCH>) block_norm_bwd(const NormArgs a, int G) {
     constexpr int V = Vec<T>::N, P = Cols<T, NCH>::P, Q = LN ? 4 : 2;
     constexpr bool kSmem = P > 4, kAhead = NCH == 1;
     extern __shared__ float4 smem4[];   // one vector: parameters, then the reduction of small groups; else the sums
@@ -461,43 +521,44 @@ __global__ void __launch_bounds__(sizeof(T) == 4 && NCH == 1 ? 640 : kMaxThreads
         cols.get(raw[4], d);
         at_next = at + stride * a.D;
         if (kAhead) cols.load(in, at_next, row + stride < a.rows, raw);
-        float r_b = 1.f;
-        if (a.post != JFA_NORM_NONE) r_b = normalise<T, NCH, LN>(b, a.post, cols, g, inv_d, a.eps);   // b: hat of the block
-        gate_values<P, true>(a.gate_kind, u, slope);                                              // u: act(u)
+        gate_values<P, true>(a.gate_kind, u, slope);   // u: act(u)
+        float mu;
+        const float r_b = to_y<T, NCH, LN>(par, W1, LN ? W0 : 0, a.post, a.pre, cols, g, inv_d, a.eps, b, y, u, mu);
+        float2 w[P];
         if (pre) {
-            float2 w[P];
+            const bool layer = LN && a.pre == JFA_NORM_LAYER;
+            if (layer) {
+                shift_by<P>(y, -mu);
+                cols.mask(y);
+            }
+            if (LN)
 #pragma unroll
-            for (int i = 0; i < P; ++i) w[i] = b[i];
-            scale_shift<P, LN>(par, W1, LN ? W0 : 0, w);
-#pragma unroll
-            for (int i = 0; i < P; ++i) y[i] = fma2(u[i], w[i], y[i]);
-            const float r_y = normalise<T, NCH, LN>(y, a.pre, cols, g, inv_d, a.eps);             // y: hat of y
-            float2 c1 = both(0.f), c2 = both(0.f);
+                for (int i = 0; i < P; ++i) sums.add(LN ? Q_PRE0 : 0, i, dn[i]);
+            // g = dn * gamma; with y = c of the norm, hat = r c:
+            //   d += r (g - hat mean(g hat) - mean(g)), the two sums with that of c^2
             par.get(Q1, w);
+#pragma unroll
+            for (int i = 0; i < P; ++i) w[i] = mul2(dn[i], w[i]);
+            float s[LN ? 3 : 2] = {dot<P>(y, y), dot<P>(w, y)};
+            if (LN) s[LN ? 2 : 0] = plain_sum<P>(w);
+            g.template sum<LN ? 3 : 2>(s);
+            const float r_y = rsqrtf(fmaf(s[0], inv_d, a.eps));
+            scale_by<P>(y, r_y);
+            const float2 c1 = both(-r_y * s[1] * inv_d);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 sums.fma(Q_PRE1, i, dn[i], y[i]);
-                if (LN) sums.add(LN ? Q_PRE0 : 0, i, dn[i]);
-                dn[i] = mul2(dn[i], w[i]);
-                c1 = fma2(dn[i], y[i], c1);
-                if (LN) c2 = add2(c2, dn[i]);
+                w[i] = fma2(y[i], c1, w[i]);
             }
-            const float2 c = g.template sum<LN>(c1.x + c1.y, c2.x + c2.y);
-            c1 = both(-c.x * inv_d);
-#pragma unroll
-            for (int i = 0; i < P; ++i) dn[i] = fma2(y[i], c1, dn[i]);
-            if (LN && a.pre == JFA_NORM_LAYER) {
-                c2 = both(-c.y * inv_d);
-#pragma unroll
-                for (int i = 0; i < P; ++i) dn[i] = add2(dn[i], c2);
-                cols.mask(dn);   // no part in the sums below
+            if (layer) {
+                shift_by<P>(w, -s[LN ? 2 : 0] * inv_d);
+                cols.mask(w);   // no part in the sums below
             }
 #pragma unroll
-            for (int i = 0; i < P; ++i) d[i] = fma2(both(r_y), dn[i], d[i]);
+            for (int i = 0; i < P; ++i) d[i] = fma2(both(r_y), w[i], d[i]);
         }
         // d is dx; on to the block: dp, the gate's gradient and the sums
         if (live) cols.store(a.dx, at, d);
-        float2 w[P];
         if (gated) {
 #pragma unroll
             for (int i = 0; i < P; ++i) w[i] = b[i];
@@ -506,7 +567,6 @@ __global__ void __launch_bounds__(sizeof(T) == 4 && NCH == 1 ? 640 : kMaxThreads
             for (int i = 0; i < P; ++i) slope[i] = mul2(mul2(d[i], slope[i]), w[i]);
             if (live) cols.store(a.dgate, at, slope);
         }
-        float2 c1 = both(0.f), c2 = both(0.f);
         par.get(W1, w);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -514,19 +574,16 @@ __global__ void __launch_bounds__(sizeof(T) == 4 && NCH == 1 ? 640 : kMaxThreads
             sums.fma(Q_POST1, i, d[i], b[i]);
             if (LN) sums.add(LN ? Q_POST0 : 0, i, d[i]);
             d[i] = mul2(d[i], w[i]);
-            c1 = fma2(d[i], b[i], c1);
-            if (LN) c2 = add2(c2, d[i]);
         }
         if (a.post != JFA_NORM_NONE) {
-            const float2 c = g.template sum<LN>(c1.x + c1.y, c2.x + c2.y);
-            c1 = both(-c.x * inv_d);
-            c2 = both(LN && a.post == JFA_NORM_LAYER ? -c.y * inv_d : 0.f);
+            float s[LN ? 2 : 1] = {dot<P>(d, b)};
+            if (LN) s[LN ? 1 : 0] = plain_sum<P>(d);
+            g.template sum<LN ? 2 : 1>(s);
+            const float2 c1 = both(-s[0] * inv_d);
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                d[i] = fma2(b[i], c1, d[i]);
-                if (LN) d[i] = add2(d[i], c2);
-                d[i] = mul2(d[i], both(r_b));
-            }
+            for (int i = 0; i < P; ++i) d[i] = fma2(b[i], c1, d[i]);
+            if (LN && a.post == JFA_NORM_LAYER) shift_by<P>(d, -s[LN ? 1 : 0] * inv_d);
+            scale_by<P>(d, r_b);
         }
         if (live) cols.store(a.dblock, at, d);
     }

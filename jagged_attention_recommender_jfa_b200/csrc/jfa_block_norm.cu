@@ -351,7 +351,9 @@ __device__ __forceinline__ float to_y(const Par& par, int W1, int W0, int post, 
     if (LN && post == JFA_NORM_LAYER) {
         float s[1] = {plain_sum<P>(b)};
         g.template sum<1>(s);
-        shift_by<P>(b, -s[0] / (float)cols.D);   // exact for a constant row of exact sum
+        // s / D, corrected to the last place: exact for a constant row of exact sum
+        const float mu = s[0] * inv_d;
+        shift_by<P>(b, -fmaf(fmaf(-mu, (float)cols.D, s[0]), inv_d, mu));
         cols.mask(b);
     }
     float2 w[P];
@@ -449,11 +451,17 @@ __global__ void __launch_bounds__(kFwdBound<T, NCH>) block_norm_fwd(const NormAr
 enum { Q_POST1 = 0, Q_PRE1, Q_POST0, Q_PRE0, Q_COUNT };   // S1 of the two norms, S2 of the two
 
 // The sums over rows, in pairs: in registers, or in shared memory (each thread
-// its own columns) where a thread has so many elements that registers run out.
+// its own) where registers run out: several vectors per thread, and the four
+// sums of a LayerNorm (222283 x 1024 bf16: 1366 us in registers, with spills,
+// 1189 us in shared memory; 9001 x 1003 fp32: 103 and 89 us).
+template <typename T, int NCH, bool LN>
+constexpr bool kSumsInSmem = NCH * Vec<T>::N > 8 || LN;
+template <bool LN>
+constexpr int kBwdParams = LN ? 3 : 2;
 template <int P, int Q, bool SMEM>
 struct Sums {
     float2 v[Q][P];
-    __device__ __forceinline__ Sums(float*, const Group&) {
+    __device__ __forceinline__ Sums(float*) {
 #pragma unroll
         for (int q = 0; q < Q; ++q)
 #pragma unroll
@@ -467,7 +475,7 @@ template <int P, int Q>
 struct Sums<P, Q, true> {
     float2* mine;
     int stride;
-    __device__ __forceinline__ Sums(float* smem, const Group& g) : mine(reinterpret_cast<float2*>(smem) + g.t), stride(g.G) {
+    __device__ __forceinline__ Sums(float* smem) : mine(reinterpret_cast<float2*>(smem) + threadIdx.x), stride(blockDim.x) {
         for (int i = 0; i < Q * P; ++i) mine[i * stride] = both(0.f);
     }
     __device__ __forceinline__ void add(int q, int i, float2 x) {
@@ -484,13 +492,13 @@ struct Sums<P, Q, true> {
 template <typename T, int NCH, bool LN>
 __global__ void __launch_bounds__(kBwdBound<T, NCH>) block_norm_bwd(const NormArgs a, int G) {
     constexpr int V = Vec<T>::N, P = Cols<T, NCH>::P, Q = LN ? 4 : 2;
-    constexpr bool kSmem = P > 4, kAhead = NCH == 1;
-    extern __shared__ float4 smem4[];   // one vector: parameters, then the reduction of small groups; else the sums
+    constexpr bool kSmem = kSumsInSmem<T, NCH, LN>, kAhead = NCH == 1;
+    extern __shared__ float4 smem4[];   // parameters, sums, each where they are kept here; at the end the small groups' reduction
     float* const smem = reinterpret_cast<float*>(smem4);
     __shared__ GroupBuf buf;
     Group g(G, &buf);
-    Params<LN ? 3 : 2, P, NCH == 1> par(smem);
-    Sums<P, Q, kSmem> sums(smem, g);
+    Params<kBwdParams<LN>, P, NCH == 1> par(smem);
+    Sums<P, Q, kSmem> sums(smem + (NCH == 1 ? kBwdParams<LN> * 2 * P * blockDim.x : 0));
     const int groups = blockDim.x / G;
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t base = (int64_t)blockIdx.x * groups, row = base + threadIdx.x / G;
@@ -517,8 +525,13 @@ __global__ void __launch_bounds__(kBwdBound<T, NCH>) block_norm_bwd(const NormAr
         cols.get(raw[0], b);
         cols.get(raw[1], y);
         cols.get(raw[2], u);
-        cols.get(raw[3], dn);
-        cols.get(raw[4], d);
+        // dn and dy wait as they came (half the registers in bf16)
+        uint4 later[2][NCH];
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch) {
+            later[0][ch] = raw[3][ch];
+            later[1][ch] = raw[4][ch];
+        }
         at_next = at + stride * a.D;
         if (kAhead) cols.load(in, at_next, row + stride < a.rows, raw);
         gate_values<P, true>(a.gate_kind, u, slope);   // u: act(u)
@@ -531,6 +544,7 @@ __global__ void __launch_bounds__(kBwdBound<T, NCH>) block_norm_bwd(const NormAr
                 shift_by<P>(y, -mu);
                 cols.mask(y);
             }
+            cols.get(later[0], dn);
             if (LN)
 #pragma unroll
                 for (int i = 0; i < P; ++i) sums.add(LN ? Q_PRE0 : 0, i, dn[i]);
@@ -554,8 +568,11 @@ __global__ void __launch_bounds__(kBwdBound<T, NCH>) block_norm_bwd(const NormAr
                 shift_by<P>(w, -s[LN ? 2 : 0] * inv_d);
                 cols.mask(w);   // no part in the sums below
             }
+            cols.get(later[1], d);
 #pragma unroll
             for (int i = 0; i < P; ++i) d[i] = fma2(both(r_y), w[i], d[i]);
+        } else {
+            cols.get(later[1], d);
         }
         // d is dx; on to the block: dp, the gate's gradient and the sums
         if (live) cols.store(a.dx, at, d);
@@ -599,17 +616,18 @@ __global__ void __launch_bounds__(kBwdBound<T, NCH>) block_norm_bwd(const NormAr
     if (groups == 1) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) put(part + q * a.D, q);
-    } else if (!kSmem) {
+    } else {
         // the groups' sums in group order, through shared memory [groups][D]
-        // (behind the last use of the parameters)
+        // behind the parameters and sums
+        float* const area = smem + ((NCH == 1 ? kBwdParams<LN> : 0) + (kSmem ? Q : 0)) * 2 * P * blockDim.x;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             __syncthreads();
-            put(smem + (threadIdx.x / G) * a.D, q);
+            put(area + (threadIdx.x / G) * a.D, q);
             __syncthreads();
             for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
                 float s = 0.f;
-                for (int k = 0; k < groups; ++k) s += smem[k * a.D + c];
+                for (int k = 0; k < groups; ++k) s += area[k * a.D + c];
                 part[q * a.D + c] = s;
             }
         }
@@ -778,9 +796,9 @@ cudaError_t bwd_launch(const NormArgs& a, int* parts, cudaStream_t st) {
                                   : s.nch == 2 ? block_norm_bwd<T, 2, LN>
                                                : block_norm_bwd<T, kMostChunks<T>, LN>;
     const int pairs = s.nch * Vec<T>::N / 2;
-    size_t smem = pairs > 4 ? sizeof(float2) * Q * pairs * s.G : 0;   // the sums
-    if (s.nch == 1) smem = Params<LN ? 3 : 2, Vec<T>::N / 2, true>::bytes(s.threads);
-    if (s.groups > 1 && smem < sizeof(float) * s.groups * a.D) smem = sizeof(float) * s.groups * a.D;
+    const bool in_smem = s.nch == 1 ? kSumsInSmem<T, 1, LN> : (s.nch == 2 ? kSumsInSmem<T, 2, LN> : true);
+    const size_t smem = sizeof(float2) * pairs * s.threads * ((s.nch == 1 ? kBwdParams<LN> : 0) + (in_smem ? Q : 0)) +
+                        (s.groups > 1 ? sizeof(float) * s.groups * a.D : 0);
     cudaError_t e = allow_smem(kern, smem);
     if (e == cudaSuccess) e = row_grid(kern, s, a.rows, smem, kMaxParts, parts);
     if (e != cudaSuccess) return e;

@@ -47,15 +47,38 @@ __device__ __forceinline__ float scale_value(int byte) {
     return byte > 0 ? __uint_as_float((uint32_t)byte << 23) : __uint_as_float(1u << 22);
 }
 
-// Two E2M1 codes in a byte, `lo` in the low four bits: round to nearest even,
-// saturating at 6.
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+// Eight values times s as E2M1 codes, four bits each, value 0 lowest: round to
+// nearest even, saturating at 6.
+__device__ __forceinline__ uint32_t pack8(const float (&f)[8], float s) {
+    uint32_t o;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(o)
+        : "f"(f[0] * s), "f"(f[1] * s), "f"(f[2] * s), "f"(f[3] * s), "f"(f[4] * s), "f"(f[5] * s), "f"(f[6] * s),
+          "f"(f[7] * s));
+    return o;
 }
-__device__ __forceinline__ float2 unpack2(uint32_t byte) {
-    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// The eight values of codes, times s (exact).
+__device__ __forceinline__ void unpack8(uint32_t codes, float s, float (&f)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        f[2 * i] = v.x * s;
+        f[2 * i + 1] = v.y * s;
+    }
 }
-
 }  // namespace mx4
 }  // namespace jfa

@@ -20,38 +20,56 @@ namespace jfa {
 namespace {
 
 using mx4::inv_scale;
-using mx4::pack2;
+using mx4::pack8;
 using mx4::scale_byte;
 using mx4::scale_value;
 using mx4::scale_word;
-using mx4::unpack2;
+using mx4::unpack8;
 
-// Eight consecutive elements as floats, and the bits of their largest
-// magnitude as an fp32 number (infinities and NaN compare above every finite
-// number, so an exponent field of 255 survives the maximum).
-__device__ __forceinline__ uint32_t load8(const __nv_bfloat16* p, float (&f)[8]) {
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p));
-    const __nv_bfloat162* p2 = reinterpret_cast<const __nv_bfloat162*>(&raw);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const float2 v = __bfloat1622float2(p2[u]);
-        f[2 * u] = v.x;
-        f[2 * u + 1] = v.y;
+// Eight consecutive elements as they lie in memory; as floats; and the bits of
+// their largest magnitude as an fp32 number (infinities and NaN compare above
+// every finite number, so an exponent field of 255 survives the maximum).
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ uint32_t max_bits() const {
+        // the magnitudes' bit patterns order like the magnitudes
+        const uint32_t k = 0x7FFF7FFFu;
+        const uint32_t m = __vmaxu2(__vmaxu2(r.x & k, r.y & k), __vmaxu2(r.z & k, r.w & k));
+        return max(m << 16, m & 0xFFFF0000u);
     }
-    uint32_t m = 0;
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(f[u]) & 0x7FFFFFFFu);
-    return m;
-}
-__device__ __forceinline__ uint32_t load8(const float* p, float (&f)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    uint32_t m = 0;
+        for (int u = 0; u < 4; ++u) {
+            f[2 * u] = __uint_as_float(w[u] << 16);
+            f[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u);
+        }
+    }
+};
+template <>
+struct Raw8<float> {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    __device__ __forceinline__ uint32_t max_bits() const {
+        float f[8];
+        get(f);
+        uint32_t m = 0;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(f[u]) & 0x7FFFFFFFu);
-    return m;
-}
+        for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(f[u]) & 0x7FFFFFFFu);
+        return m;
+    }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
     uint4 o;
     uint32_t* w = reinterpret_cast<uint32_t*>(&o);
@@ -70,10 +88,33 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
 // Work unit of the row kernels: a segment, 128 columns (four blocks, one
 // scale word) of one row.  Segments of rows up to the next multiple of 128
 // are visited too: those behind the last row only write their zero scale
-// word, so that every byte of the scale tiles is defined.
-constexpr int kSegsPerHalfWarp = 4;
+// word, so that every byte of the scale tiles is defined.  A CTA takes
+// consecutive segments; a worker (half warp or warp) takes every W-th of them
+// and steps its row and column tile along (one division per worker).
 constexpr int kRowThreads = 256;
-constexpr int kSegsVec = kRowThreads / 16 * kSegsPerHalfWarp;   // segments per CTA
+constexpr int kSegsPerWorker = 4;
+
+struct Segment {
+    int64_t r;
+    int kt;
+    int dr, dk, tiles_k;
+    __device__ __forceinline__ Segment(int64_t seg0, int first, int workers, int tiles) : tiles_k(tiles) {
+        r = seg0 / tiles;
+        const unsigned at = (unsigned)(seg0 - r * tiles) + first;
+        r += at / (unsigned)tiles;
+        kt = (int)(at % (unsigned)tiles);
+        dr = (unsigned)workers / (unsigned)tiles;
+        dk = workers - dr * tiles;
+    }
+    __device__ __forceinline__ void next() {
+        r += dr;
+        kt += dk;
+        if (kt >= tiles_k) {
+            kt -= tiles_k;
+            ++r;
+        }
+    }
+};
 
 // cols % 8 == 0: sixteen lanes take a segment, eight elements (16 or 32 bytes)
 // each; the loads of a half warp's four segments are all in flight before the
@@ -83,69 +124,83 @@ __global__ void __launch_bounds__(kRowThreads) mx4_rows_vec(const T* __restrict_
                                                             int64_t segs, int tiles_k,
                                                             uint8_t* __restrict__ codes, int code_pitch,
                                                             uint8_t* __restrict__ scales, T* __restrict__ y) {
+    constexpr int kWorkers = kRowThreads / 16;
     const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
-    const int64_t seg0 = (int64_t)blockIdx.x * kSegsVec;
-    const int64_t row0 = seg0 / tiles_k;
-    const int kt0 = (int)(seg0 - row0 * tiles_k);
-    float f[kSegsPerHalfWarp][8];
-    uint32_t m[kSegsPerHalfWarp];
+    const int64_t seg0 = (int64_t)blockIdx.x * (kWorkers * kSegsPerWorker);
+    const Segment start(seg0, half, kWorkers, tiles_k);
+    Raw8<T> raw[kSegsPerWorker];
+    Segment s = start;
 #pragma unroll
-    for (int i = 0; i < kSegsPerHalfWarp; ++i) {
-        const unsigned at = (unsigned)(kt0 + i * (kRowThreads / 16) + half);
-        const int64_t r = row0 + at / (unsigned)tiles_k;
-        const int c = (int)(at % (unsigned)tiles_k) * 128 + lane * 8;
-        m[i] = 0;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) f[i][u] = 0.f;
-        if (r < rows && c < cols) m[i] = load8(x + r * cols + c, f[i]);
+    for (int i = 0; i < kSegsPerWorker; ++i, s.next()) {
+        const int c = s.kt * 128 + lane * 8;
+        if (s.r < rows && c < cols) raw[i].load(x + s.r * cols + c);
     }
+    s = start;
 #pragma unroll
-    for (int i = 0; i < kSegsPerHalfWarp; ++i) {
-        const int local = i * (kRowThreads / 16) + half;
-        const unsigned at = (unsigned)(kt0 + local);
-        const int64_t r = row0 + at / (unsigned)tiles_k;
-        const int kt = (int)(at % (unsigned)tiles_k), c = kt * 128 + lane * 8;
-        uint32_t mx = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int b = scale_byte(mx);
-        const float s = inv_scale(b);
-        uint32_t code = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) code |= pack2(f[i][2 * u] * s, f[i][2 * u + 1] * s) << (8 * u);
-        if (b == mx4::kNanScale) code = 0;
-        // the word of the segment's four scale bytes, in every fourth lane's byte
-        uint32_t word = (uint32_t)b << (8 * (lane >> 2));
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        if (seg0 + local >= segs) continue;
-        if (lane == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(r, kt, tiles_k)) = word;
-        if (r >= rows) continue;
-        if (c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + r * code_pitch + c / 2) = code;
+    for (int i = 0; i < kSegsPerWorker; ++i, s.next()) {
+        const int c = s.kt * 128 + lane * 8;
+        uint32_t m = raw[i].max_bits();
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int b = scale_byte(m);
+        float f[8];
+        raw[i].get(f);
+        const uint32_t code = b == mx4::kNanScale ? 0u : pack8(f, inv_scale(b));
+        if (seg0 + i * kWorkers + half >= segs) continue;
+        if ((lane & 3) == 0) scales[scale_word(s.r, s.kt, tiles_k) + (lane >> 2)] = (uint8_t)b;
+        if (s.r >= rows) continue;
+        if (c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + s.r * code_pitch + c / 2) = code;
         if (DEQ && c < cols) {
-            const float back = scale_value(b);
             float d[8];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float2 v = unpack2((code >> (8 * u)) & 0xFF);
-                d[2 * u] = v.x * back;
-                d[2 * u + 1] = v.y * back;
-            }
-            store8(y + r * cols + c, d);
+            unpack8(code, scale_value(b), d);
+            store8(y + s.r * cols + c, d);
         }
     }
 }
 
-// Any width: a warp takes a segment, lane l the element l of each of its four
-// blocks (rows need not be aligned; a warp's load is 32 consecutive elements).
-// The block maximum is one warp reduction; codes are packed by a shuffle with
-// the neighbour (two codes to a byte) and a 4 x 4 byte transpose among the
-// even lanes of eight, after which each holds four bytes of one block.
-constexpr int kSegsPerWarp = 4;
-constexpr int kSegsAny = kRowThreads / 32 * kSegsPerWarp;
+// Any width.  A segment starts `shift` elements behind a 16-byte boundary; lane
+// l loads the aligned vectors from that boundary on (8 elements' worth), takes
+// the first vector of lane l + 1, and shifts its own eight elements out of the
+// two.  The dequantised copy goes the other way: each lane puts together the
+// aligned vectors that start in its elements' place from its own and the last
+// of lane l - 1, and only the ends of a segment go element by element.
+// The window of W words that starts `half` half words into w.
+template <int W>
+__device__ __forceinline__ void window(const uint32_t (&w)[W + 4], int half, uint32_t (&o)[W]) {
+    uint32_t a[W + 2], b[W + 1];
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) a[i] = half & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) b[i] = half & 2 ? a[i + 1] : a[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i) o[i] = half & 1 ? __byte_perm(b[i], b[i + 1], 0x5432) : b[i];
+}
 
-__device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) {
-    return __bfloat162float(__ushort_as_bfloat16(__ldg(reinterpret_cast<const unsigned short*>(p))));
+template <typename T>
+__device__ __forceinline__ void from_words(const uint32_t (&w)[2 * sizeof(T)], float (&f)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        if (sizeof(T) == 4) f[u] = __uint_as_float(w[sizeof(T) == 4 ? u : 0]);
+        else f[u] = __uint_as_float(u & 1 ? (w[u / 2] & 0xFFFF0000u) : (w[u / 2] << 16));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void to_words(const float (&f)[8], uint32_t (&w)[2 * sizeof(T)]) {
+#pragma unroll
+    for (int i = 0; i < (int)(2 * sizeof(T)); ++i) {
+        if (sizeof(T) == 4) {
+            w[i] = __float_as_uint(f[i]);
+        } else {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f[(2 * i) & 7], f[(2 * i + 1) & 7]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+    }
+}
+// Element u of packed words, as stored.
+template <typename T, int W>
+__device__ __forceinline__ void put_element(T* p, const uint32_t (&w)[W], int u) {
+    if (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(p) = w[sizeof(T) == 4 ? u : 0];
+    else *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[sizeof(T) == 4 ? 0 : u / 2] >> (16 * (u & 1)));
 }
 
 template <typename T, bool DEQ>
@@ -153,54 +208,101 @@ __global__ void __launch_bounds__(kRowThreads) mx4_rows_any(const T* __restrict_
                                                             int64_t segs, int tiles_k,
                                                             uint8_t* __restrict__ codes, int code_pitch,
                                                             uint8_t* __restrict__ scales, T* __restrict__ y) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t seg0 = (int64_t)blockIdx.x * kSegsAny;
-    const int64_t row0 = seg0 / tiles_k;
-    const int kt0 = (int)(seg0 - row0 * tiles_k);
-    float f[kSegsPerWarp][4];
+    constexpr int kWorkers = kRowThreads / 16, kSegs = 2;
+    constexpr int V = 16 / sizeof(T), N = 8 / V, W = 4 * N;   // elements of a vector, vectors and words of eight elements
+    const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
+    const int64_t seg0 = (int64_t)blockIdx.x * (kWorkers * kSegs), total = rows * cols;
+    const Segment start(seg0, half, kWorkers, tiles_k);
+    uint32_t w[kSegs][W + 4];
+    Segment s = start;
 #pragma unroll
-    for (int i = 0; i < kSegsPerWarp; ++i) {
-        const unsigned at = (unsigned)(kt0 + i * (kRowThreads / 32) + warp);
-        const int64_t r = row0 + at / (unsigned)tiles_k;
-        const int c = (int)(at % (unsigned)tiles_k) * 128 + lane;
+    for (int i = 0; i < kSegs; ++i, s.next()) {
+        const int shift = (int)((s.r * cols) % V), first = s.kt * 128 - shift + lane * 8;   // column of the lane's first vector
+        const int64_t off = s.r * cols + first;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[i][j] = (r < rows && c + 32 * j < cols) ? load1(x + r * cols + c + 32 * j) : 0.f;
-    }
+        for (int n = 0; n <= N; ++n) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            const int64_t at = off + n * V;
+            // the last lane also needs the vector behind its own
+            if (s.r < rows && first + n * V < cols && (n < N || lane == 15)) {
+                if (at + V <= total) {
+                    v = __ldg(reinterpret_cast<const uint4*>(x + at));
+                } else {
+                    T* e = reinterpret_cast<T*>(&v);   // the tensor ends inside this vector
 #pragma unroll
-    for (int i = 0; i < kSegsPerWarp; ++i) {
-        const int local = i * (kRowThreads / 32) + warp;
-        if (seg0 + local >= segs) return;   // whole warps leave together
-        const unsigned at = (unsigned)(kt0 + local);
-        const int64_t r = row0 + at / (unsigned)tiles_k;
-        const int kt = (int)(at % (unsigned)tiles_k);
-        uint32_t word = 0, four = 0;   // scale bytes; this lane's four codes, a byte each
-        int b[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            b[j] = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(f[i][j]) & 0x7FFFFFFFu));
-            word |= (uint32_t)b[j] << (8 * j);
-            const uint32_t code = b[j] == mx4::kNanScale ? 0u : pack2(f[i][j] * inv_scale(b[j]), 0.f);
-            four |= code << (8 * j);
+                    for (int u = 0; u < V; ++u)
+                        if (at + u < total) e[u] = x[at + u];
+                }
+            }
+            w[i][4 * n] = v.x;
+            w[i][4 * n + 1] = v.y;
+            w[i][4 * n + 2] = v.z;
+            w[i][4 * n + 3] = v.w;
         }
-        if (lane == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(r, kt, tiles_k)) = word;
-        if (r >= rows) continue;
-        // even lanes: byte j = codes (2i, 2i + 1) of block j
-        const uint32_t pair = four | (__shfl_down_sync(0xffffffffu, four, 1) << 4);
-        // transpose among lanes 0, 2, 4, 6 of eight: lane 2q ends with block q's
-        // bytes.  First the 2 x 2 blocks of bytes (lanes 4 apart), then within
-        // them (lanes 2 apart).
-        const int q = (lane >> 1) & 3;
-        uint32_t o = __shfl_xor_sync(0xffffffffu, pair, 4);
-        uint32_t t = (q & 2) ? __byte_perm(o, pair, 0x7632) : __byte_perm(pair, o, 0x5410);
-        o = __shfl_xor_sync(0xffffffffu, t, 2);
-        t = (q & 1) ? __byte_perm(o, t, 0x7351) : __byte_perm(t, o, 0x6240);
-        const int byte = kt * 64 + q * 16 + (lane >> 3) * 4;
-        if ((lane & 1) == 0 && byte < code_pitch) *reinterpret_cast<uint32_t*>(codes + r * code_pitch + byte) = t;
-        if (DEQ) {
+    }
+    s = start;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = kt * 128 + 32 * j + lane;
-                if (c < cols) y[r * cols + c] = from_f<T>(unpack2((four >> (8 * j)) & 0xF).x * scale_value(b[j]));
+    for (int i = 0; i < kSegs; ++i, s.next()) {
+        const int shift = (int)((s.r * cols) % V);
+        const int c = s.kt * 128 + lane * 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t next = __shfl_down_sync(0xffffffffu, w[i][k], 1, 16);
+            if (lane < 15) w[i][W + k] = next;
+        }
+        uint32_t mine[W];
+        window<W>(w[i], shift * (int)sizeof(T) / 2, mine);
+        float f[8];
+        from_words<T>(mine, f);
+        if (c + 8 > cols) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (c + u >= cols) f[u] = 0.f;   // the next row's
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(f[u]) & 0x7FFFFFFFu);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int b = scale_byte(m);
+        const uint32_t code = b == mx4::kNanScale ? 0u : pack8(f, inv_scale(b));
+        const bool live = seg0 + i * kWorkers + half < segs;
+        if (live && (lane & 3) == 0) scales[scale_word(s.r, s.kt, tiles_k) + (lane >> 2)] = (uint8_t)b;
+        if (live && s.r < rows && c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + s.r * code_pitch + c / 2) = code;
+        if (DEQ) {
+            float d[8];
+            unpack8(code, scale_value(b), d);
+            uint32_t both[W + 4], out[W];   // the last vector of lane - 1, then this lane's
+            to_words<T>(d, mine);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) both[k] = __shfl_up_sync(0xffffffffu, mine[W - 4 + k], 1, 16);
+#pragma unroll
+            for (int k = 0; k < W; ++k) both[4 + k] = mine[k];
+            if (shift == 0) {
+#pragma unroll
+                for (int k = 0; k < W; ++k) out[k] = mine[k];
+            } else {
+                window<W>(both, 8 - shift * (int)sizeof(T) / 2, out);
+            }
+            if (!live || s.r >= rows) continue;
+            const int lim = min(cols, s.kt * 128 + 128);
+            T* const row = y + s.r * cols;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int e = c - shift + n * V;
+                if (e >= s.kt * 128 && e + V <= lim) {
+                    *reinterpret_cast<uint4*>(row + e) = make_uint4(out[4 * n], out[4 * n + 1], out[4 * n + 2], out[4 * n + 3]);
+                } else if (e < lim) {
+#pragma unroll
+                    for (int u = 0; u < V; ++u)
+                        if (e + u >= s.kt * 128 && e + u < lim) put_element<T, W>(row + e + u, out, n * V + u);
+                }
+            }
+            // the last lane's elements behind its last aligned vector
+            if (lane == 15 && shift != 0) {
+#pragma unroll
+                for (int u = 8 - V + 1; u < 8; ++u)
+                    if (u >= 8 - shift && c + u < lim) put_element<T, W>(row + c + u, mine, u);
             }
         }
     }
@@ -272,10 +374,10 @@ __global__ void __launch_bounds__(512 / CPT) mx4_cols(const T* __restrict__ x, i
         const float s = inv_scale(b[i]);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            uint32_t o = 0;
+            float f[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) o |= pack2(v[8 * w + 2 * u].get(i) * s, v[8 * w + 2 * u + 1].get(i) * s) << (8 * u);
-            code[i][w] = b[i] == mx4::kNanScale ? 0u : o;
+            for (int u = 0; u < 8; ++u) f[u] = v[8 * w + u].get(i);
+            code[i][w] = b[i] == mx4::kNanScale ? 0u : pack8(f, s);
         }
         *reinterpret_cast<uint4*>(s_codes + (cl + i) * kStagePitch + blk * 16) =
             make_uint4(code[i][0], code[i][1], code[i][2], code[i][3]);
@@ -285,11 +387,13 @@ __global__ void __launch_bounds__(512 / CPT) mx4_cols(const T* __restrict__ x, i
         T* p = y + r0 * cols + c;
         const float k0 = scale_value(b[0]), k1 = scale_value(b[CPT - 1]);
 #pragma unroll
-        for (int t = 0; t < 32; t += 2) {
-            const float2 a0 = unpack2((code[0][t >> 3] >> (4 * (t & 7))) & 0xFF);
-            const float2 a1 = unpack2((code[CPT - 1][t >> 3] >> (4 * (t & 7))) & 0xFF);
-            if (t < n) Cols<T, CPT>::store(p + (int64_t)t * cols, a0.x * k0, a1.x * k1);
-            if (t + 1 < n) Cols<T, CPT>::store(p + (int64_t)(t + 1) * cols, a0.y * k0, a1.y * k1);
+        for (int w = 0; w < 4; ++w) {
+            float d0[8], d1[8];
+            unpack8(code[0][w], k0, d0);
+            unpack8(code[CPT - 1][w], k1, d1);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (8 * w + u < n) Cols<T, CPT>::store(p + (int64_t)(8 * w + u) * cols, d0[u], d1[u]);
         }
     }
     __syncthreads();
@@ -314,7 +418,7 @@ cudaError_t launch_rows(const T* x, int64_t rows, int cols, uint8_t* codes, uint
     const int64_t segs = mx4::scale_tiles_r(rows) * 128 * tiles_k;
     const int pitch = (int)(mx4::padded_cols(cols) / 2);
     const bool vec = cols % 8 == 0;
-    const int64_t per = vec ? kSegsVec : kSegsAny;
+    const int64_t per = (vec ? kSegsPerWorker : 2) * kRowThreads / 16;
     const int64_t grid = (segs + per - 1) / per;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     prof_begin(st);

@@ -43,7 +43,7 @@ struct Shape {
     static constexpr uint32_t kStage = kA + kB + kSfA + kSfB;
     static constexpr int kStages = BN == 128 ? 7 : 5;
     static constexpr uint32_t kRing = kStages * kStage;
-    static constexpr uint32_t kSmem = kRing + kEpiWarps * kStageBytes + 1024;
+    static constexpr uint32_t kSmem = kRing + kEpiWarps * (kStageBytes + kWarpCols * 4) + 1024;
     static constexpr bool kShared = BN == 256;                     // the accumulators share columns
     static constexpr uint32_t kAccStride = 128;                   // TMEM columns from one accumulator to the other
     static constexpr uint32_t kSfCol = kAccStride + BN;            // a slot of scale columns per ring stage
@@ -70,19 +70,13 @@ enum { OUT_ANY = 0, OUT_BF16 = 1, OUT_F32 = 2, OUT_F32_ADD = 3 };
 // columns) is staged with the 128-byte swizzle (a row's 16-byte pieces in
 // different banks for consecutive lanes) and leaves as one TMA store, which
 // also cuts off what lies behind the last row and column; fp32 sums into the
-// result are TMA reductions (one addition per element).  The first version
+// result are TMA reductions (one addition per element).  `bias`: the box's
+// columns' in shared memory, or NULL.  The first version
 // stored each lane's row piece from registers, 32 rows per instruction: the
 // read-out then took 4900 cycles per 256 x 192 tile.
-__device__ __forceinline__ void add_bias(const Mx4Params& P, float (&v)[32], int col0) {
-    if (!P.bias) return;
-#pragma unroll
-    for (int t = 0; t < 32; ++t)
-        if (col0 + t < P.n) v[t] += __ldg(P.bias + col0 + t);
-}
-
 template <int OUT>
 __device__ __forceinline__ void store_box(const Mx4Params& P, const uint32_t* r, int row0, int col0, int lane,
-                                          uint32_t stage) {
+                                          uint32_t stage, const float* bias) {
     if (row0 >= P.m || col0 >= P.n) return;   // nothing of the box lies inside
     if (lane == 0) mx4::bulk_wait_read();
     __syncwarp();
@@ -92,7 +86,13 @@ __device__ __forceinline__ void store_box(const Mx4Params& P, const uint32_t* r,
         float v[32];
 #pragma unroll
         for (int t = 0; t < 32; ++t) v[t] = __uint_as_float(r[32 * h + t]);
-        add_bias(P, v, col0 + 32 * h);
+        if (bias) {
+#pragma unroll
+            for (int t = 0; t < 32; t += 4) {
+                const float4 b = *reinterpret_cast<const float4*>(bias + 32 * h + t);   // the same for all lanes
+                v[t] += b.x; v[t + 1] += b.y; v[t + 2] += b.z; v[t + 3] += b.w;
+            }
+        }
 #pragma unroll
         for (int q = 0; q < (OUT == OUT_BF16 ? 4 : 8); ++q) {
             uint4 w;
@@ -297,10 +297,18 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) mx4_gemm_pair(const __
     } else {
         const int quarter = warp & 3, group = warp >> 2;   // TMEM lanes; columns
         uint8_t* const stage = smem + S::kRing + warp * kStageBytes;
+        float* const bias = reinterpret_cast<float*>(smem + S::kRing + S::kEpiWarps * kStageBytes) + warp * S::kWarpCols;
         int turn = 0;
         for (int tile = first; tile < tiles; tile += step, ++turn) {
             const int row0 = (tile / n_tiles) * 256 + (int)rank * 128 + quarter * 32;
             const int col0 = (tile % n_tiles) * BN + group * S::kWarpCols;
+            if (OUT != OUT_ANY && P.bias) {
+                // while the tile is computed: this warp's columns of the bias
+                __syncwarp();
+#pragma unroll
+                for (int t = lane; t < S::kWarpCols; t += 32) bias[t] = col0 + t < P.n ? __ldg(P.bias + col0 + t) : 0.f;
+                __syncwarp();
+            }
             // lane 0 waits for the warp
             int up = 0;
             if (lane == 0) up = mbar_wait(&bars.acc_full[turn & 1], (turn >> 1) & 1, abort_flag, P.hdr) ? 1 : 0;
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) mx4_gemm_pair(const __
 #pragma unroll
             for (int i = 0; i < kChunks; i += OUT == OUT_BF16 ? 2 : 1) {
                 if (OUT == OUT_ANY) store_any(P, r[i], row0, col0 + i * 32, lane, reinterpret_cast<float*>(stage));
-                else store_box<OUT>(P, r[i], row0, col0 + i * 32, lane, smem_u32(stage));
+                else store_box<OUT>(P, r[i], row0, col0 + i * 32, lane, smem_u32(stage), P.bias ? bias + i * 32 : nullptr);
             }
         }
         if (OUT != OUT_ANY && lane == 0) mx4::bulk_wait();

@@ -711,7 +711,12 @@ def block_norm_backward(desc: jfa_block_norm, x, block, gate=None, scale=None, p
             _invalid(f"ws: device {ws.device}, expected {x.device}")
         g = {"x": torch.empty_like(x), "block": torch.empty_like(x),
              "gate": None if gate is None else torch.empty_like(x)}
-        g.update({k: None if p is None else torch.empty_like(p) for k, p in params.items()})
+        # the parameters' gradients: rows of one small buffer, each on 16 bytes
+        dim = desc.dim
+        sums = torch.empty((len(params), (dim + 3) // 4 * 4), dtype=torch.float32, device=x.device)
+        if dim % 4:
+            sums = sums[:, :dim]
+        g.update({k: None if p is None else r for (k, p), r in zip(params.items(), sums.unbind(0))})
         _check(load().jfa_block_norm_backward(
             ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), _ptr(scale),
             _ptr(post_gamma), _ptr(post_beta), _ptr(pre_gamma), _ptr(pre_beta), _ptr(dy), _ptr(dn),

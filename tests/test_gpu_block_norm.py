@@ -197,3 +197,42 @@ def test_graph_capture_and_streams(cuda_device):
         torch.cuda.synchronize()
         assert torch.equal(y, y_r) and torch.equal(n, n_r)
         assert all(torch.equal(g[k], g_r[k]) for k in g if g[k] is not None)
+
+
+@pytest.mark.parametrize("dim", [64, 101, 1024, 1027])
+def test_bad_values_stay_in_their_row(cuda_device, dim):
+    kw, up = make(9, dim, "bf16", "rms", "layer", "silu", seed=1)
+    kw, up = dev_(kw, cuda_device), dev_(up, cuda_device)
+    desc = jfa.make_block_norm(rows=9, dim=dim, post_norm="rms", pre_norm="layer")
+    y, n = jfa.block_norm_forward(desc, **kw)
+    g = jfa.block_norm_backward(desc, **kw, **up)
+    for where, value in (("block", float("nan")), ("x", float("inf")), ("gate", float("-inf"))):
+        bad = {k: None if t is None else t.clone() for k, t in kw.items()}
+        bad[where][4, dim - 1] = value
+        by, bn = jfa.block_norm_forward(desc, **bad)
+        bg = jfa.block_norm_backward(desc, **bad, **up)
+        keep = [i for i in range(9) if i != 4]
+        assert torch.equal(by[keep], y[keep]) and torch.equal(bn[keep], n[keep])
+        assert all(torch.equal(bg[k][keep], g[k][keep]) for k in ("x", "block", "gate"))
+        assert torch.isnan(bn[4]).any()
+
+
+def test_offsets_past_32_bits(cuda_device):
+    # 2.3e9 elements: the last rows against the same rows alone
+    rows, dim = 2_240_001, 1024
+    x, b, u = (torch.empty(rows, dim, dtype=torch.bfloat16, device=cuda_device) for _ in range(3))
+    for i, t in enumerate((x, b, u)):
+        t[-64:] = torch.randn(64, dim, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).to(cuda_device)
+        t[:-64] = 0
+    p = torch.ones(dim, device=cuda_device)
+    kw = dict(scale=p, post_gamma=p, pre_gamma=p)
+    y, n = jfa.block_norm_forward(jfa.make_block_norm(rows=rows, dim=dim), x, b, u, **kw)
+    small = jfa.make_block_norm(rows=64, dim=dim)
+    cut = [t[-64:].clone() for t in (x, b, u)]
+    ys, ns = jfa.block_norm_forward(small, *cut, **kw)
+    assert torch.equal(y[-64:], ys) and torch.equal(n[-64:], ns) and (y[:-64] == 0).all()
+    del y, n
+    g = jfa.block_norm_backward(jfa.make_block_norm(rows=rows, dim=dim), x, b, u, dy=x, dn=b, **kw)
+    gs = jfa.block_norm_backward(small, *cut, dy=cut[0], dn=cut[1], **kw)
+    for k in ("x", "block", "gate"):
+        assert torch.equal(g[k][-64:], gs[k])

@@ -275,3 +275,38 @@ def test_streams_and_graph_capture(cuda_device):
         torch.cuda.synchronize()
         assert torch.equal(y, ref)
     jfa.jfa_check_error(ws)
+
+
+@pytest.mark.parametrize("along_rows", [False, True])
+def test_quantise_offsets_past_32_bits(cuda_device, along_rows):
+    # 2.2e9 elements: the last rows (of whole scale tiles) against the same rows alone
+    rows, cols = 2_240_000, 1000
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=cuda_device)
+    x[-128:] = torch.randn(128, cols, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(cuda_device)
+    assert rows % 128 == 0 and rows * cols > 1 << 31
+    op, deq = jfa.quantize_mxfp4(x, along_rows, want_dequant=True)
+    alone, d = jfa.quantize_mxfp4(x[-128:].clone(), along_rows, want_dequant=True)
+    assert torch.equal(deq[-128:], d) and (deq[:-128] == 0).all()
+    if along_rows:
+        assert torch.equal(op.codes[:, -64:], alone.codes)
+        at = op.scales.view(8, rows // 128, 512)
+        assert torch.equal(at[:, -1].reshape(-1), alone.scales)
+    else:
+        assert torch.equal(op.codes[-128:], alone.codes)
+        assert torch.equal(op.scales[-alone.scales.numel():], alone.scales)
+
+
+def test_product_offsets_past_32_bits(cuda_device):
+    # 2.3e9 results; the last rows against the same rows alone
+    m, n, k = 560_128, 4096, 64
+    x = draw(256, k, "bf16", 1).to(cuda_device)
+    w = jfa.quantize_mxfp4(draw(n, k, "bf16", 2).to(cuda_device))
+    big = torch.zeros(m, k, dtype=torch.bfloat16, device=cuda_device)
+    big[-256:] = x
+    ref = jfa.matmul_mxfp4(jfa.quantize_mxfp4(x), w)
+    out = jfa.matmul_mxfp4(jfa.quantize_mxfp4(big), w)
+    assert torch.equal(out[-256:], ref) and (out[:-256] == 0).all()
+    odd = torch.zeros(m, 4097, dtype=torch.bfloat16, device=cuda_device)   # rows off every boundary
+    w1 = jfa.quantize_mxfp4(torch.cat([draw(n, k, "bf16", 2), draw(1, k, "bf16", 3)]).to(cuda_device))
+    jfa.matmul_mxfp4(jfa.quantize_mxfp4(big), w1, out=odd)
+    assert torch.equal(odd[-256:, :4096], ref) and (odd[:-256] == 0).all()

@@ -7,6 +7,8 @@
 #include <cuda_fp4.h>
 #include <stdint.h>
 
+#include "jfa_sm100.cuh"
+
 namespace jfa {
 
 constexpr int64_t kMx4MaxDim = (int64_t)1 << 30;   // rows and columns of an operand
@@ -24,6 +26,19 @@ __host__ __device__ inline int64_t scale_tiles_r(int64_t rows) { return (rows + 
 // each, in the order tcgen05.cp spreads over 32 lanes x 16 bytes.
 __host__ __device__ inline int64_t scale_word(int64_t r, int64_t kt, int64_t tiles_k) {
     return ((r >> 7) * tiles_k + kt) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
+
+// Largest magnitude, a NaN if there is one: exponent field 255 then, as for an
+// infinity.
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                         __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&m);
 }
 
 // Scale byte of a block from the bits of its largest magnitude:
@@ -49,8 +64,15 @@ __device__ __forceinline__ float scale_value(int byte) {
 
 // Eight values times s as E2M1 codes, four bits each, value 0 lowest: round to
 // nearest even, saturating at 6.
-__device__ __forceinline__ uint32_t pack8(const float (&f)[8], float s) {
+__device__ __forceinline__ uint32_t pack8(const float (&g)[8], float s) {
     uint32_t o;
+    float f[8];
+#pragma unroll
+    for (int u = 0; u < 8; u += 2) {
+        const float2 v = sm100::mul2(make_float2(g[u], g[u + 1]), make_float2(s, s));
+        f[u] = v.x;
+        f[u + 1] = v.y;
+    }
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
@@ -58,8 +80,7 @@ __device__ __forceinline__ uint32_t pack8(const float (&f)[8], float s) {
         "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
         "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(o)
-        : "f"(f[0] * s), "f"(f[1] * s), "f"(f[2] * s), "f"(f[3] * s), "f"(f[4] * s), "f"(f[5] * s), "f"(f[6] * s),
-          "f"(f[7] * s));
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
     return o;
 }
 // The eight values of codes, times s (exact).
@@ -76,8 +97,9 @@ __device__ __forceinline__ void unpack8(uint32_t codes, float s, float (&f)[8]) 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        f[2 * i] = v.x * s;
-        f[2 * i + 1] = v.y * s;
+        const float2 p = sm100::mul2(v, make_float2(s, s));
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
     }
 }
 }  // namespace mx4

@@ -19,6 +19,8 @@ namespace jfa {
 
 namespace {
 
+using mx4::absmax3;
+using mx4::absmax_bf16x2;
 using mx4::inv_scale;
 using mx4::pack8;
 using mx4::scale_byte;
@@ -36,10 +38,8 @@ struct Raw8<__nv_bfloat16> {
     uint4 r = make_uint4(0u, 0u, 0u, 0u);
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ uint32_t max_bits() const {
-        // the magnitudes' bit patterns order like the magnitudes
-        const uint32_t k = 0x7FFF7FFFu;
-        const uint32_t m = __vmaxu2(__vmaxu2(r.x & k, r.y & k), __vmaxu2(r.z & k, r.w & k));
-        return max(m << 16, m & 0xFFFF0000u);
+        const uint32_t m = absmax_bf16x2(absmax_bf16x2(r.x, r.y), absmax_bf16x2(r.z, r.w));
+        return max(m << 16, m & 0xFFFF0000u);   // bits of magnitudes order like the magnitudes
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -62,12 +62,7 @@ struct Raw8<float> {
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     }
     __device__ __forceinline__ uint32_t max_bits() const {
-        float f[8];
-        get(f);
-        uint32_t m = 0;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(f[u]) & 0x7FFFFFFFu);
-        return m;
+        return __float_as_uint(absmax3(absmax3(a.x, a.y, a.z), absmax3(a.w, b.x, b.y), absmax3(b.z, b.w, 0.f)));
     }
 };
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
@@ -259,9 +254,7 @@ __global__ void __launch_bounds__(kRowThreads) mx4_rows_any(const T* __restrict_
             for (int u = 0; u < 8; ++u)
                 if (c + u >= cols) f[u] = 0.f;   // the next row's
         }
-        uint32_t m = 0;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(f[u]) & 0x7FFFFFFFu);
+        uint32_t m = __float_as_uint(absmax3(absmax3(f[0], f[1], f[2]), absmax3(f[3], f[4], f[5]), absmax3(f[6], f[7], 0.f)));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const int b = scale_byte(m);
@@ -323,6 +316,13 @@ struct Cols<__nv_bfloat16, 2> {
     uint32_t raw = 0;
     __device__ void load(const __nv_bfloat16* p) { raw = __ldg(reinterpret_cast<const unsigned int*>(p)); }
     __device__ float get(int i) const { return __uint_as_float(i ? (raw & 0xFFFF0000u) : (raw << 16)); }
+    __device__ static void max_bits(const Cols (&v)[32], uint32_t (&m)[2]) {
+        uint32_t k = 0;
+#pragma unroll
+        for (int t = 0; t < 32; ++t) k = absmax_bf16x2(k, v[t].raw);
+        m[0] = k << 16;
+        m[1] = k & 0xFFFF0000u;
+    }
     __device__ static void store(__nv_bfloat16* p, float a, float b) {
         *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
     }
@@ -332,6 +332,12 @@ struct Cols<__nv_bfloat16, 1> {
     uint32_t raw = 0;
     __device__ void load(const __nv_bfloat16* p) { raw = __ldg(reinterpret_cast<const unsigned short*>(p)); }
     __device__ float get(int) const { return __uint_as_float(raw << 16); }
+    __device__ static void max_bits(const Cols (&v)[32], uint32_t (&m)[1]) {
+        uint32_t k = 0;
+#pragma unroll
+        for (int t = 0; t < 32; ++t) k = absmax_bf16x2(k, v[t].raw);
+        m[0] = k << 16;
+    }
     __device__ static void store(__nv_bfloat16* p, float a, float) { *p = __float2bfloat16_rn(a); }
 };
 template <>
@@ -339,6 +345,12 @@ struct Cols<float, 1> {
     float raw = 0.f;
     __device__ void load(const float* p) { raw = __ldg(p); }
     __device__ float get(int) const { return raw; }
+    __device__ static void max_bits(const Cols (&v)[32], uint32_t (&m)[1]) {
+        float k = 0.f;
+#pragma unroll
+        for (int t = 0; t < 32; t += 2) k = absmax3(k, v[t].raw, v[t + 1].raw);
+        m[0] = __float_as_uint(k);
+    }
     __device__ static void store(float* p, float a, float) { *p = a; }
 };
 
@@ -363,14 +375,12 @@ __global__ void __launch_bounds__(512 / CPT) mx4_cols(const T* __restrict__ x, i
         for (int t = 0; t < 32; ++t)
             if (t < n) v[t].load(p + (int64_t)t * cols);
     }
-    uint32_t code[CPT][4];
+    uint32_t code[CPT][4], amax[CPT];
     int b[CPT];
+    Cols<T, CPT>::max_bits(v, amax);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int t = 0; t < 32; ++t) m = max(m, __float_as_uint(v[t].get(i)) & 0x7FFFFFFFu);
-        b[i] = scale_byte(m);
+        b[i] = scale_byte(amax[i]);
         const float s = inv_scale(b[i]);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {

@@ -21,13 +21,6 @@ inline int64_t padded_cols(int64_t cols) { return (cols + 31) / 32 * 32; }
 __host__ __device__ inline int64_t scale_tiles_k(int64_t cols) { return (cols + 127) / 128; }
 __host__ __device__ inline int64_t scale_tiles_r(int64_t rows) { return (rows + 127) / 128; }
 
-// Byte offset of the 4-byte word that holds the scales of row r, columns
-// [128 kt, 128 kt + 128): tiles of 128 rows x 4 scales, 512 contiguous bytes
-// each, in the order tcgen05.cp spreads over 32 lanes x 16 bytes.
-__host__ __device__ inline int64_t scale_word(int64_t r, int64_t kt, int64_t tiles_k) {
-    return ((r >> 7) * tiles_k + kt) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
-}
-
 // Largest magnitude, a NaN if there is one: exponent field 255 then, as for an
 // infinity.
 __device__ __forceinline__ float absmax3(float a, float b, float c) {

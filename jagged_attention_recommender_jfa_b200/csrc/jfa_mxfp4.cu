@@ -25,7 +25,6 @@ using mx4::inv_scale;
 using mx4::pack8;
 using mx4::scale_byte;
 using mx4::scale_value;
-using mx4::scale_word;
 using mx4::unpack8;
 
 // Eight consecutive elements as they lie in memory; as floats; and the bits of
@@ -80,60 +79,55 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
     reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// Work unit of the row kernels: a segment, 128 columns (four blocks, one
-// scale word) of one row.  Segments of rows up to the next multiple of 128
-// are visited too: those behind the last row only write their zero scale
-// word, so that every byte of the scale tiles is defined.  A CTA takes
-// consecutive segments; a worker (half warp or warp) takes every W-th of them
-// and steps its row and column tile along (one division per worker).
-constexpr int kRowThreads = 256;
-constexpr int kSegsPerWorker = 4;
+// A CTA of the row kernels takes 128 rows x 128 columns: one scale tile, whose
+// 512 bytes leave together (those of rows and blocks behind the tensor as
+// zeros).  Sixteen lanes take a segment (the tile's part of a row), eight
+// elements each; the loads of a half warp's four segments are all in flight
+// before the first conversion.  The first version walked the segments in
+// memory order and stored each scale byte by itself: 12% of its time.
+constexpr int kRowThreads = 512;
+constexpr int kHalves = kRowThreads / 16, kSegs = 128 / kHalves;
 
-struct Segment {
-    int64_t r;
-    int kt;
-    int dr, dk, tiles_k;
-    __device__ __forceinline__ Segment(int64_t seg0, int first, int workers, int tiles) : tiles_k(tiles) {
-        r = seg0 / tiles;
-        const unsigned at = (unsigned)(seg0 - r * tiles) + first;
-        r += at / (unsigned)tiles;
-        kt = (int)(at % (unsigned)tiles);
-        dr = (unsigned)workers / (unsigned)tiles;
-        dk = workers - dr * tiles;
-    }
-    __device__ __forceinline__ void next() {
-        r += dr;
-        kt += dk;
-        if (kt >= tiles_k) {
-            kt -= tiles_k;
-            ++r;
-        }
+// CTAs an SM should hold (registers): 222283 x 1024 bf16 with the copy at 2 / 3 /
+// 4: 179 / 156 / 160 us; fp32 has twice the bytes per thread in flight.
+template <typename T>
+constexpr int kRowCtas = sizeof(T) == 2 ? 3 : 2;
+
+struct RowTile {
+    int64_t r0;   // first row
+    int kt;       // column tile
+    __device__ __forceinline__ RowTile(int tiles_k) {
+        const unsigned rt = blockIdx.x / (unsigned)tiles_k;
+        r0 = (int64_t)rt * 128;
+        kt = (int)(blockIdx.x - rt * (unsigned)tiles_k);
     }
 };
+// The scale byte of block j of row i of the tile, staged as it is stored.
+__device__ __forceinline__ int staged_scale(int i, int j) { return (i & 31) * 16 + (i >> 5) * 4 + j; }
+__device__ __forceinline__ void store_scale_tile(const uint8_t* staged, uint8_t* scales) {
+    __syncthreads();
+    if (threadIdx.x < 32)
+        reinterpret_cast<uint4*>(scales + (int64_t)blockIdx.x * 512)[threadIdx.x] = reinterpret_cast<const uint4*>(staged)[threadIdx.x];
+}
 
-// cols % 8 == 0: sixteen lanes take a segment, eight elements (16 or 32 bytes)
-// each; the loads of a half warp's four segments are all in flight before the
-// first conversion.
+// cols % 8 == 0: a lane's eight elements are 16 or 32 aligned bytes.
 template <typename T, bool DEQ>
-__global__ void __launch_bounds__(kRowThreads) mx4_rows_vec(const T* __restrict__ x, int64_t rows, int cols,
-                                                            int64_t segs, int tiles_k,
-                                                            uint8_t* __restrict__ codes, int code_pitch,
-                                                            uint8_t* __restrict__ scales, T* __restrict__ y) {
-    constexpr int kWorkers = kRowThreads / 16;
+__global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_rows_vec(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
+                                                                         uint8_t* __restrict__ codes, int code_pitch,
+                                                                         uint8_t* __restrict__ scales, T* __restrict__ y) {
+    __shared__ __align__(16) uint8_t staged[512];
     const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
-    const int64_t seg0 = (int64_t)blockIdx.x * (kWorkers * kSegsPerWorker);
-    const Segment start(seg0, half, kWorkers, tiles_k);
-    Raw8<T> raw[kSegsPerWorker];
-    Segment s = start;
+    const RowTile tile(tiles_k);
+    const int c = tile.kt * 128 + lane * 8;
+    Raw8<T> raw[kSegs];
 #pragma unroll
-    for (int i = 0; i < kSegsPerWorker; ++i, s.next()) {
-        const int c = s.kt * 128 + lane * 8;
-        if (s.r < rows && c < cols) raw[i].load(x + s.r * cols + c);
+    for (int i = 0; i < kSegs; ++i) {
+        const int64_t r = tile.r0 + i * kHalves + half;
+        if (r < rows && c < cols) raw[i].load(x + r * cols + c);
     }
-    s = start;
 #pragma unroll
-    for (int i = 0; i < kSegsPerWorker; ++i, s.next()) {
-        const int c = s.kt * 128 + lane * 8;
+    for (int i = 0; i < kSegs; ++i) {
+        const int64_t r = tile.r0 + i * kHalves + half;
         uint32_t m = raw[i].max_bits();
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -141,16 +135,16 @@ __global__ void __launch_bounds__(kRowThreads) mx4_rows_vec(const T* __restrict_
         float f[8];
         raw[i].get(f);
         const uint32_t code = b == mx4::kNanScale ? 0u : pack8(f, inv_scale(b));
-        if (seg0 + i * kWorkers + half >= segs) continue;
-        if ((lane & 3) == 0) scales[scale_word(s.r, s.kt, tiles_k) + (lane >> 2)] = (uint8_t)b;
-        if (s.r >= rows) continue;
-        if (c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + s.r * code_pitch + c / 2) = code;
+        if ((lane & 3) == 0) staged[staged_scale(i * kHalves + half, lane >> 2)] = (uint8_t)b;
+        if (r >= rows) continue;
+        if (c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + r * code_pitch + c / 2) = code;
         if (DEQ && c < cols) {
             float d[8];
             unpack8(code, scale_value(b), d);
-            store8(y + s.r * cols + c, d);
+            store8(y + r * cols + c, d);
         }
     }
+    store_scale_tile(staged, scales);
 }
 
 // Any width.  A segment starts `shift` elements behind a 16-byte boundary; lane
@@ -199,106 +193,109 @@ __device__ __forceinline__ void put_element(T* p, const uint32_t (&w)[W], int u)
 }
 
 template <typename T, bool DEQ>
-__global__ void __launch_bounds__(kRowThreads) mx4_rows_any(const T* __restrict__ x, int64_t rows, int cols,
-                                                            int64_t segs, int tiles_k,
-                                                            uint8_t* __restrict__ codes, int code_pitch,
-                                                            uint8_t* __restrict__ scales, T* __restrict__ y) {
-    constexpr int kWorkers = kRowThreads / 16, kSegs = 2;
+__global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_rows_any(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
+                                                                         uint8_t* __restrict__ codes, int code_pitch,
+                                                                         uint8_t* __restrict__ scales, T* __restrict__ y) {
     constexpr int V = 16 / sizeof(T), N = 8 / V, W = 4 * N;   // elements of a vector, vectors and words of eight elements
+    constexpr int kBatch = 2;                                 // segments under way at a time
+    __shared__ __align__(16) uint8_t staged[512];
     const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
-    const int64_t seg0 = (int64_t)blockIdx.x * (kWorkers * kSegs), total = rows * cols;
-    const Segment start(seg0, half, kWorkers, tiles_k);
-    uint32_t w[kSegs][W + 4];
-    Segment s = start;
+    const int64_t total = rows * cols;
+    const RowTile tile(tiles_k);
+    const int c = tile.kt * 128 + lane * 8;
+#pragma unroll 1
+    for (int i0 = 0; i0 < kSegs; i0 += kBatch) {
+        uint32_t w[kBatch][W + 4];
 #pragma unroll
-    for (int i = 0; i < kSegs; ++i, s.next()) {
-        const int shift = (int)((s.r * cols) % V), first = s.kt * 128 - shift + lane * 8;   // column of the lane's first vector
-        const int64_t off = s.r * cols + first;
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t r = tile.r0 + (i0 + i) * kHalves + half;
+            const int shift = (int)((r * cols) % V), first = c - shift;   // column of the lane's first vector
+            const int64_t off = r * cols + first;
 #pragma unroll
-        for (int n = 0; n <= N; ++n) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            const int64_t at = off + n * V;
-            // the last lane also needs the vector behind its own
-            if (s.r < rows && first + n * V < cols && (n < N || lane == 15)) {
-                if (at + V <= total) {
-                    v = __ldg(reinterpret_cast<const uint4*>(x + at));
+            for (int n = 0; n <= N; ++n) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                const int64_t at = off + n * V;
+                // the last lane also needs the vector behind its own
+                if (r < rows && first + n * V < cols && (n < N || lane == 15)) {
+                    if (at + V <= total) {
+                        v = __ldg(reinterpret_cast<const uint4*>(x + at));
+                    } else {
+                        T* e = reinterpret_cast<T*>(&v);   // the tensor ends inside this vector
+#pragma unroll
+                        for (int u = 0; u < V; ++u)
+                            if (at + u < total) e[u] = x[at + u];
+                    }
+                }
+                w[i][4 * n] = v.x;
+                w[i][4 * n + 1] = v.y;
+                w[i][4 * n + 2] = v.z;
+                w[i][4 * n + 3] = v.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t r = tile.r0 + (i0 + i) * kHalves + half;
+            const int shift = (int)((r * cols) % V);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t next = __shfl_down_sync(0xffffffffu, w[i][k], 1, 16);
+                if (lane < 15) w[i][W + k] = next;
+            }
+            uint32_t mine[W];
+            window<W>(w[i], shift * (int)sizeof(T) / 2, mine);
+            float f[8];
+            from_words<T>(mine, f);
+            if (c + 8 > cols) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (c + u >= cols) f[u] = 0.f;   // the next row's
+            }
+            uint32_t m = __float_as_uint(absmax3(absmax3(f[0], f[1], f[2]), absmax3(f[3], f[4], f[5]), absmax3(f[6], f[7], 0.f)));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const int b = scale_byte(m);
+            const uint32_t code = b == mx4::kNanScale ? 0u : pack8(f, inv_scale(b));
+            if ((lane & 3) == 0) staged[staged_scale((i0 + i) * kHalves + half, lane >> 2)] = (uint8_t)b;
+            if (r < rows && c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + r * code_pitch + c / 2) = code;
+            if (DEQ) {
+                float d[8];
+                unpack8(code, scale_value(b), d);
+                uint32_t both[W + 4], out[W];   // the last vector of lane - 1, then this lane's
+                to_words<T>(d, mine);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) both[k] = __shfl_up_sync(0xffffffffu, mine[W - 4 + k], 1, 16);
+#pragma unroll
+                for (int k = 0; k < W; ++k) both[4 + k] = mine[k];
+                if (shift == 0) {
+#pragma unroll
+                    for (int k = 0; k < W; ++k) out[k] = mine[k];
                 } else {
-                    T* e = reinterpret_cast<T*>(&v);   // the tensor ends inside this vector
-#pragma unroll
-                    for (int u = 0; u < V; ++u)
-                        if (at + u < total) e[u] = x[at + u];
+                    window<W>(both, 8 - shift * (int)sizeof(T) / 2, out);
                 }
-            }
-            w[i][4 * n] = v.x;
-            w[i][4 * n + 1] = v.y;
-            w[i][4 * n + 2] = v.z;
-            w[i][4 * n + 3] = v.w;
-        }
-    }
-    s = start;
+                if (r >= rows) continue;
+                const int lim = min(cols, tile.kt * 128 + 128);
+                T* const row = y + r * cols;
 #pragma unroll
-    for (int i = 0; i < kSegs; ++i, s.next()) {
-        const int shift = (int)((s.r * cols) % V);
-        const int c = s.kt * 128 + lane * 8;
+                for (int n = 0; n < N; ++n) {
+                    const int e = c - shift + n * V;
+                    if (e >= tile.kt * 128 && e + V <= lim) {
+                        *reinterpret_cast<uint4*>(row + e) = make_uint4(out[4 * n], out[4 * n + 1], out[4 * n + 2], out[4 * n + 3]);
+                    } else if (e < lim) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t next = __shfl_down_sync(0xffffffffu, w[i][k], 1, 16);
-            if (lane < 15) w[i][W + k] = next;
-        }
-        uint32_t mine[W];
-        window<W>(w[i], shift * (int)sizeof(T) / 2, mine);
-        float f[8];
-        from_words<T>(mine, f);
-        if (c + 8 > cols) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (c + u >= cols) f[u] = 0.f;   // the next row's
-        }
-        uint32_t m = __float_as_uint(absmax3(absmax3(f[0], f[1], f[2]), absmax3(f[3], f[4], f[5]), absmax3(f[6], f[7], 0.f)));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int b = scale_byte(m);
-        const uint32_t code = b == mx4::kNanScale ? 0u : pack8(f, inv_scale(b));
-        const bool live = seg0 + i * kWorkers + half < segs;
-        if (live && (lane & 3) == 0) scales[scale_word(s.r, s.kt, tiles_k) + (lane >> 2)] = (uint8_t)b;
-        if (live && s.r < rows && c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + s.r * code_pitch + c / 2) = code;
-        if (DEQ) {
-            float d[8];
-            unpack8(code, scale_value(b), d);
-            uint32_t both[W + 4], out[W];   // the last vector of lane - 1, then this lane's
-            to_words<T>(d, mine);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) both[k] = __shfl_up_sync(0xffffffffu, mine[W - 4 + k], 1, 16);
-#pragma unroll
-            for (int k = 0; k < W; ++k) both[4 + k] = mine[k];
-            if (shift == 0) {
-#pragma unroll
-                for (int k = 0; k < W; ++k) out[k] = mine[k];
-            } else {
-                window<W>(both, 8 - shift * (int)sizeof(T) / 2, out);
-            }
-            if (!live || s.r >= rows) continue;
-            const int lim = min(cols, s.kt * 128 + 128);
-            T* const row = y + s.r * cols;
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const int e = c - shift + n * V;
-                if (e >= s.kt * 128 && e + V <= lim) {
-                    *reinterpret_cast<uint4*>(row + e) = make_uint4(out[4 * n], out[4 * n + 1], out[4 * n + 2], out[4 * n + 3]);
-                } else if (e < lim) {
-#pragma unroll
-                    for (int u = 0; u < V; ++u)
-                        if (e + u >= s.kt * 128 && e + u < lim) put_element<T, W>(row + e + u, out, n * V + u);
+                        for (int u = 0; u < V; ++u)
+                            if (e + u >= tile.kt * 128 && e + u < lim) put_element<T, W>(row + e + u, out, n * V + u);
+                    }
                 }
-            }
-            // the last lane's elements behind its last aligned vector
-            if (lane == 15 && shift != 0) {
+                // the last lane's elements behind its last aligned vector
+                if (lane == 15 && shift != 0) {
 #pragma unroll
-                for (int u = 8 - V + 1; u < 8; ++u)
-                    if (u >= 8 - shift && c + u < lim) put_element<T, W>(row + c + u, mine, u);
+                    for (int u = 8 - V + 1; u < 8; ++u)
+                        if (u >= 8 - shift && c + u < lim) put_element<T, W>(row + c + u, mine, u);
+                }
             }
         }
     }
+    store_scale_tile(staged, scales);
 }
 
 // The operand of the transpose: blocks are 32 consecutive rows of a column.
@@ -354,8 +351,13 @@ struct Cols<float, 1> {
     __device__ static void store(float* p, float a, float) { *p = a; }
 };
 
+// CTAs an SM should hold: one column per thread 2 / 3: 207 / 193 us (222283 x
+// 1023 bf16), two columns 3 / 4: 111 / 117 us without the copy, 214 / 195 with it.
+template <int CPT, bool DEQ>
+constexpr int kColCtas = CPT == 2 && DEQ ? 4 : 3;
+
 template <typename T, int CPT, bool DEQ>
-__global__ void __launch_bounds__(512 / CPT) mx4_cols(const T* __restrict__ x, int64_t rows, int cols,
+__global__ void __launch_bounds__(512 / CPT, kColCtas<CPT, DEQ>) mx4_cols(const T* __restrict__ x, int64_t rows, int cols,
                                                       int col_tiles, int64_t blocks_k, int64_t tiles_k,
                                                       uint8_t* __restrict__ codes,
                                                       uint8_t* __restrict__ scales, T* __restrict__ y) {
@@ -425,15 +427,12 @@ __global__ void __launch_bounds__(512 / CPT) mx4_cols(const T* __restrict__ x, i
 template <typename T, bool DEQ>
 cudaError_t launch_rows(const T* x, int64_t rows, int cols, uint8_t* codes, uint8_t* scales, T* y, cudaStream_t st) {
     const int tiles_k = (int)mx4::scale_tiles_k(cols);
-    const int64_t segs = mx4::scale_tiles_r(rows) * 128 * tiles_k;
+    const int64_t grid = mx4::scale_tiles_r(rows) * tiles_k;
     const int pitch = (int)(mx4::padded_cols(cols) / 2);
-    const bool vec = cols % 8 == 0;
-    const int64_t per = (vec ? kSegsPerWorker : 2) * kRowThreads / 16;
-    const int64_t grid = (segs + per - 1) / per;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     prof_begin(st);
-    if (vec) mx4_rows_vec<T, DEQ><<<(unsigned)grid, kRowThreads, 0, st>>>(x, rows, cols, segs, tiles_k, codes, pitch, scales, y);
-    else mx4_rows_any<T, DEQ><<<(unsigned)grid, kRowThreads, 0, st>>>(x, rows, cols, segs, tiles_k, codes, pitch, scales, y);
+    if (cols % 8 == 0) mx4_rows_vec<T, DEQ><<<(unsigned)grid, kRowThreads, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y);
+    else mx4_rows_any<T, DEQ><<<(unsigned)grid, kRowThreads, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y);
     prof_end(st, K_MX4_ROWS);
     return cudaGetLastError();
 }

@@ -62,7 +62,6 @@ struct Profiler {
 thread_local Profiler g_prof;
 thread_local char g_msg[512] = "";
 thread_local int g_test_hook = 0;       // jfa_test_inject: armed for the next forward
-constexpr int kTestWaitLimitUs = 5000;  // the injected failure's wait limit
 
 const char* const kKernelNames[K_COUNT] = {
     "sched_prepare", "sched_rank", "simt_fwd", "simt_bwd_pre", "simt_bwd_dq", "simt_bwd_dkdv",
@@ -80,6 +79,12 @@ jfa_status set_last_error(jfa_status s, const char* fmt, ...) {
     vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
     va_end(ap);
     return s;
+}
+
+int take_test_hook(int what) {
+    if (g_test_hook != what) return 0;
+    g_test_hook = 0;
+    return 1;
 }
 
 void prof_begin(cudaStream_t st) {
@@ -461,7 +466,7 @@ jfa_status jfa_schedule(const jfa_problem* problem, const int32_t* q_offsets,
 }
 
 jfa_status jfa_test_inject(int what) {
-    if (what != 0 && what != JFA_TEST_FWD_SKIP_LOAD)
+    if (what != 0 && what != JFA_TEST_FWD_SKIP_LOAD && what != JFA_TEST_MATMUL_SKIP_LOAD)
         return fail(JFA_ERR_INVALID_ARGUMENT, "unknown test injection %d", what);
     g_test_hook = what;
     return JFA_OK;

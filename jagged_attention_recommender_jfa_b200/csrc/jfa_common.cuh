@@ -195,6 +195,10 @@ enum KernelId {
 void prof_begin(cudaStream_t st);
 void prof_end(cudaStream_t st, int kernel_id);
 
+// 1, and disarmed, if jfa_test_inject armed this thread with `what`.
+int take_test_hook(int what);
+constexpr int kTestWaitLimitUs = 5000;   // the injected failure's wait limit
+
 // Records the thread-local message jfa_last_error() returns and passes the
 // status through.
 jfa_status set_last_error(jfa_status s, const char* fmt, ...);

@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm(const __grid_constant__ Mx4
             const uint32_t st = base + s * S::kStage, bar = smem_u32(&bars.full[s]);
             const int kk = k0 + issued;
             mx4::expect_tx_one(one, &bars.full[s], stage_bytes);
-            mx4::tma_load_2d(one, st, &P.ta, bar, kk * 128, m0);
+            const uint32_t skip = P.test_skip_load && blockIdx.x == 0 && issued == 0;
+            mx4::tma_load_2d(skip ? 0u : one, st, &P.ta, bar, kk * 128, m0);
             mx4::tma_load_2d(one, st + S::kA, &P.tb, bar, kk * 128, n0);
             mx4::tma_load_2d(one, st + S::kA + S::kB, &P.tsa, bar, kk * 256, m0 >> 7);
             mx4::tma_load_2d(one, st + S::kA + S::kB + S::kSf, &P.tsb, bar, kk * 256, n0 >> 7);
@@ -343,9 +344,18 @@ cudaError_t mx4_product(int64_t m, int64_t n, int64_t k, const uint8_t* ac, cons
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const Plan plan = choose(m, n, P.k_stages, sms);
-    if (plan.pair) return mx4_product_pair(P, m, n, k, ac, as, bc, bs, plan.bn, sms, st);
-    return plan.bn == 64 ? launch<64>(P, m, n, k, ac, as, bc, bs, plan.split, st)
-                         : launch<128>(P, m, n, k, ac, as, bc, bs, plan.split, st);
+    P.test_skip_load = k > 0 ? take_test_hook(JFA_TEST_MATMUL_SKIP_LOAD) : 0;
+    cudaError_t e = cudaSuccess;
+    if (P.test_skip_load) {
+        static const int32_t limit = kTestWaitLimitUs;
+        e = cudaMemcpyAsync(&hdr->wait_limit_us, &limit, sizeof(limit), cudaMemcpyHostToDevice, st);
+        if (e != cudaSuccess) return e;
+    }
+    if (plan.pair) e = mx4_product_pair(P, m, n, k, ac, as, bc, bs, plan.bn, sms, st);
+    else if (plan.bn == 64) e = launch<64>(P, m, n, k, ac, as, bc, bs, plan.split, st);
+    else e = launch<128>(P, m, n, k, ac, as, bc, bs, plan.split, st);
+    if (P.test_skip_load && e == cudaSuccess) e = cudaMemsetAsync(&hdr->wait_limit_us, 0, sizeof(int32_t), st);
+    return e;
 }
 
 }  // namespace jfa

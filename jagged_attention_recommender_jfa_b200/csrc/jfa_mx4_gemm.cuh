@@ -17,6 +17,7 @@ struct Mx4Params {
     const float* bias;
     void* out;              // [m][n]
     int out_bf16, accumulate;
+    int test_skip_load;     // test hook: CTA 0 leaves out its first load, so that the bounded waits run out
     WsHeader* hdr;
 };
 

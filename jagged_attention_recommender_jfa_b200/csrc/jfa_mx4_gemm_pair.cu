@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) mx4_gemm_pair(const __
                 }
                 const uint32_t st = base + s * S::kStage, bar = full0 + s * 8;
                 mx4::expect_tx_one(arm, &bars.full[s], 2 * S::kStage);
-                mx4::tma_load_2d_pair(one, st, &P.ta, bar, kk * 128, m0);
+                const uint32_t skip = P.test_skip_load && blockIdx.x == 0 && it == 0;
+                mx4::tma_load_2d_pair(skip ? 0u : one, st, &P.ta, bar, kk * 128, m0);
                 mx4::tma_load_2d_pair(one, st + S::kA, &P.tb, bar, kk * 128, n0 + (int)rank * (BN / 2));
                 mx4::tma_load_2d_pair(one, st + S::kA + S::kB, &P.tsa, bar, kk * 256, m0 >> 7);
                 mx4::tma_load_2d_pair(one, st + S::kA + S::kB + S::kSfA, &P.tsb, bar, kk * 256, n0 >> 7);

@@ -49,7 +49,7 @@ EXPORTS = ("jfa_workspace_bytes", "jfa_forward", "jfa_backward", "jfa_quantize_m
            "jfa_block_norm_backward")
 NORM = {"none": 0, "rms": 1, "layer": 2}
 GATE = {"none": 0, "identity": 1, "silu": 2, "sigmoid": 3}
-JFA_TEST_FWD_SKIP_LOAD = 1
+JFA_TEST_FWD_SKIP_LOAD, JFA_TEST_MATMUL_SKIP_LOAD = 1, 2
 PARTITION = {"lpt": 0, "bbs": 1}
 
 

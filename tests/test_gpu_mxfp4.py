@@ -310,3 +310,20 @@ def test_product_offsets_past_32_bits(cuda_device):
     w1 = jfa.quantize_mxfp4(torch.cat([draw(n, k, "bf16", 2), draw(1, k, "bf16", 3)]).to(cuda_device))
     jfa.matmul_mxfp4(jfa.quantize_mxfp4(big), w1, out=odd)
     assert torch.equal(odd[-256:, :4096], ref) and (odd[:-256] == 0).all()
+
+
+# one CTA per tile, a split contraction over a cluster, a pair of CTAs (one
+# stage, and more than its ring holds)
+@pytest.mark.parametrize("m,n,k", [(100, 8192, 256), (64, 64, 8192), (300, 512, 256), (300, 512, 8192)])
+def test_bounded_waits_end_in_an_error(cuda_device, m, n, k):
+    # a load that never comes: the waits give up, the call reports it, and the
+    # same workspace and buffers work again
+    ws = jfa.mxfp4_workspace(cuda_device)
+    a, b = (jfa.quantize_mxfp4(draw(r, k, "bf16", r).to(cuda_device)) for r in (m, n))
+    want = jfa.matmul_mxfp4(a, b, ws=ws)
+    out = torch.empty_like(want)
+    jfa.jfa_test_inject(jfa.JFA_TEST_MATMUL_SKIP_LOAD)
+    with pytest.raises(jfa.JfaError) as ei:
+        jfa.matmul_mxfp4(a, b, out=out, ws=ws)
+    assert ei.value.status == jfa.JFA_ERR_TIMEOUT
+    assert torch.equal(jfa.matmul_mxfp4(a, b, out=out, ws=ws), want)

@@ -634,10 +634,10 @@ __global__ void __launch_bounds__(kBwdBound<T, NCH>) block_norm_bwd(const NormAr
     }
 }
 
-// Adds the partial rows (in order within sixteen interleaved strands, which
+// Adds the partial rows (in order within 32 interleaved strands, which
 // are then added in order) and forms the parameter gradients: blockIdx.y 0 the
 // block's norm and the scale, 1 the next norm.
-constexpr int kStrands = 16;
+constexpr int kStrands = 32;
 __global__ void __launch_bounds__(32 * kStrands) block_norm_sum(const NormArgs a, int n, float* dscale, float* dpost_gamma,
                                                                 float* dpost_beta, float* dpre_gamma, float* dpre_beta) {
     __shared__ float2 s_part[kStrands][32];

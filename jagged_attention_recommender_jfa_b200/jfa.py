@@ -551,19 +551,31 @@ def mxfp4_workspace(device) -> torch.Tensor:
     return torch.zeros(jfa_mxfp4_workspace_bytes(), dtype=torch.uint8, device=device)
 
 
+def _matrix(x, name="x"):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        _invalid(f"{name}: a 2-D torch tensor is needed")
+    _tensor(x, name, x.shape, _TORCH_DTYPE, None)
+    return x.shape
+
+
+def _code_pitch(cols):
+    return (cols + 31) // 32 * 16
+
+
+def _scale_bytes(rows, cols):
+    return (rows + 127) // 128 * ((cols + 127) // 128) * 512
+
+
 def quantize_mxfp4(x, along_rows=False, want_dequant=False, stream=None):
     """MXFP4 operand of ``x`` [rows, cols] (bf16 or fp32), or of its transpose
     with ``along_rows`` (blocks of 32 rows).  With ``want_dequant`` also
     returns the values it stands for, laid out like ``x``."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        _invalid("x: a 2-D torch tensor is needed")
-    _tensor(x, "x", x.shape, _TORCH_DTYPE, None)
-    rows, cols = x.shape
+    rows, cols = _matrix(x)
     r, c = (cols, rows) if along_rows else (rows, cols)
-    dev, dt = x.device, _TORCH_DTYPE[x.dtype]
-    with _on(dev, stream) as s:
-        codes = torch.empty((r, (c + 31) // 32 * 16), dtype=torch.uint8, device=dev)
-        scales = torch.empty(_scale_bytes(r, c), dtype=torch.uint8, device=dev)
+    dt, u8 = _TORCH_DTYPE[x.dtype], torch.uint8
+    with _on(x.device, stream) as s:
+        codes = x.new_empty((r, _code_pitch(c)), dtype=u8)
+        scales = x.new_empty(_scale_bytes(r, c), dtype=u8)
         if want_dequant:
             dequant = torch.empty_like(x)
             _check(load().jfa_quantize_mxfp4_dequant(
@@ -575,17 +587,29 @@ def quantize_mxfp4(x, along_rows=False, want_dequant=False, stream=None):
         return MxOperand(codes, scales, r, c)
 
 
-def _scale_bytes(rows, cols):
-    return (rows + 127) // 128 * ((cols + 127) // 128) * 512
-
-
 def _operand(o, name, device=None):
     if not isinstance(o, MxOperand):
         _invalid(f"{name}: an MxOperand is needed")
     if o.rows < 0 or o.cols < 0:
         _invalid(f"{name}: negative size")
-    _tensor(o.codes, name + ".codes", (o.rows, (o.cols + 31) // 32 * 16), _U8, device)
+    _tensor(o.codes, name + ".codes", (o.rows, _code_pitch(o.cols)), _U8, device)
     _tensor(o.scales, name + ".scales", (_scale_bytes(o.rows, o.cols),), _U8, o.codes.device)
+
+
+def _ws_on(ws, device):
+    """The caller's workspace, on the device, or a fresh one."""
+    if ws is None:
+        return mxfp4_workspace(device)
+    if ws.device != device:
+        _invalid(f"ws: device {ws.device}, expected {device}")
+    return ws
+
+
+def _product(m, n, k, a, a_scales, b: MxOperand, bias, out, accumulate, ws, s):
+    """jfa_matmul_mxfp4 on checked arguments; a and a_scales are addresses."""
+    _check(load().jfa_matmul_mxfp4(
+        m, n, k, a, a_scales, b.codes.data_ptr(), b.scales.data_ptr(), _ptr(bias), out.data_ptr(),
+        _TORCH_DTYPE[out.dtype], 1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), s))
 
 
 def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torch.bfloat16,
@@ -608,17 +632,11 @@ def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torc
         _invalid("accumulate needs out")
     elif out_dtype not in _TORCH_DTYPE:
         _invalid(f"out_dtype {out_dtype} is not one of {tuple(_TORCH_DTYPE)}")
-    if ws is not None and (not ws.is_cuda or ws.device != dev):
-        _invalid(f"ws: device {ws.device}, expected {dev}")
     with _on(dev, stream) as s:
+        ws = _ws_on(ws, dev)
         if out is None:
-            out = torch.empty((m, n), dtype=out_dtype, device=dev)
-        if ws is None:
-            ws = mxfp4_workspace(dev)
-        _check(load().jfa_matmul_mxfp4(
-            m, n, k, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
-            b.scales.data_ptr(), _ptr(bias), out.data_ptr(), _TORCH_DTYPE[out.dtype],
-            1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), s))
+            out = a.codes.new_empty((m, n), dtype=out_dtype)
+        _product(m, n, k, a.codes.data_ptr(), a.scales.data_ptr(), b, bias, out, accumulate, ws, s)
         if check:
             jfa_check_error(ws, s)
     return out
@@ -627,8 +645,26 @@ def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torc
 def linear_mxfp4_forward(x, w: MxOperand, bias=None, ws=None, stream=None, check=True):
     """``x`` [m, k] (quantised here) times the transpose of the weight operand
     ``w`` [n, k] (``quantize_mxfp4`` of the weight), in the dtype of ``x``."""
-    a = quantize_mxfp4(x, stream=stream)
-    return matmul_mxfp4(a, w, bias=bias, out_dtype=x.dtype, ws=ws, stream=stream, check=check)
+    m, k = _matrix(x)
+    dev = x.device
+    _operand(w, "w", dev)
+    n = w.rows
+    if k != w.cols:
+        _invalid(f"x has {k} columns, w {w.cols}")
+    if bias is not None:
+        _tensor(bias, "bias", (n,), _F32, dev)
+    code_bytes = m * _code_pitch(k)
+    with _on(dev, stream) as s:
+        ws = _ws_on(ws, dev)
+        buf = x.new_empty(code_bytes + _scale_bytes(m, k), dtype=torch.uint8)   # codes, then scales
+        codes = buf.data_ptr()
+        _check(load().jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 0, codes,
+                                         codes + code_bytes, s))
+        out = x.new_empty((m, n))
+        _product(m, n, k, codes, codes + code_bytes, w, bias, out, False, ws, s)
+        if check:
+            jfa_check_error(ws, s)
+    return out
 
 
 def linear_mxfp4_backward(dy, x, w_t: MxOperand, dw=None, ws=None, stream=None, check=True):
@@ -637,22 +673,38 @@ def linear_mxfp4_backward(dy, x, w_t: MxOperand, dw=None, ws=None, stream=None, 
     product of operands quantised along its own contraction (the quantiser is
     passed straight through).  ``w_t``: ``quantize_mxfp4(weight,
     along_rows=True)``.  The bias's gradient is ``dy.sum(0)``."""
-    if not (isinstance(dy, torch.Tensor) and isinstance(x, torch.Tensor) and dy.dim() == 2
-            and x.dim() == 2 and dy.shape[0] == x.shape[0]):
-        _invalid("dy [m, n] and x [m, k] are needed")
-    _operand(w_t, "w_t")
-    if w_t.rows != x.shape[1] or w_t.cols != dy.shape[1]:
-        _invalid(f"w_t is {w_t.rows} x {w_t.cols}, expected {x.shape[1]} x {dy.shape[1]}")
-    if dw is not None:
-        _tensor(dw, "dw", (dy.shape[1], x.shape[1]), _F32, dy.device)
-    if ws is None:
-        with _on(dy.device, stream):
-            ws = mxfp4_workspace(dy.device)
-    kw = dict(ws=ws, stream=stream)
-    dx = matmul_mxfp4(quantize_mxfp4(dy, stream=stream), w_t, out_dtype=dy.dtype, check=False, **kw)
-    dw = matmul_mxfp4(quantize_mxfp4(dy, along_rows=True, stream=stream),
-                      quantize_mxfp4(x, along_rows=True, stream=stream), out=dw,
-                      out_dtype=torch.float32, accumulate=dw is not None, check=check, **kw)
+    m, n = _matrix(dy, "dy")
+    _matrix(x)
+    dev, k = dy.device, x.shape[1]
+    if x.shape[0] != m or x.device != dev:
+        _invalid(f"x: {tuple(x.shape)} on {x.device} does not go with dy: {tuple(dy.shape)} on {dev}")
+    _operand(w_t, "w_t", dev)
+    if w_t.rows != k or w_t.cols != n:
+        _invalid(f"w_t is {w_t.rows} x {w_t.cols}, expected {k} x {n}")
+    accumulate = dw is not None
+    if accumulate:
+        _tensor(dw, "dw", (n, k), _F32, dev)
+    dt = _TORCH_DTYPE[dy.dtype]
+    row_codes, col_codes, pitch = m * _code_pitch(n), n * _code_pitch(m), _code_pitch(m)
+    with _on(dev, stream) as s:
+        ws = _ws_on(ws, dev)
+        lib = load()
+        # one buffer: dy's operand, then (behind the first product) its transpose's
+        buf = dy.new_empty(max(row_codes + _scale_bytes(m, n), col_codes + _scale_bytes(n, m)), dtype=torch.uint8)
+        p = buf.data_ptr()
+        _check(lib.jfa_quantize_mxfp4(dy.data_ptr(), dt, m, n, 0, p, p + row_codes, s))
+        dx = dy.new_empty((m, k))
+        _product(m, k, n, p, p + row_codes, w_t, None, dx, False, ws, s)
+        _check(lib.jfa_quantize_mxfp4(dy.data_ptr(), dt, m, n, 1, p, p + col_codes, s))
+        codes = x.new_empty((k, pitch), dtype=torch.uint8)
+        scales = x.new_empty(_scale_bytes(k, m), dtype=torch.uint8)
+        _check(lib.jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 1, codes.data_ptr(),
+                                      scales.data_ptr(), s))
+        if not accumulate:
+            dw = dy.new_empty((n, k), dtype=torch.float32)
+        _product(n, k, m, p, p + col_codes, MxOperand(codes, scales, k, m), None, dw, accumulate, ws, s)
+        if check:
+            jfa_check_error(ws, s)
     return dx, dw
 
 
@@ -670,21 +722,26 @@ def _block_norm_args(desc, x, tensors, params):
     dim, dev = desc.dim, x.device
     shape = (desc.rows, dim)
     _tensor(x, "x", shape, dt, None)
-    for name, t in tensors.items():
+    for name, t in zip(("block", "gate", "dy", "dn"), tensors):
         if t is not None:
             _tensor(t, name, shape, dt, dev)
-    for name, t in params.items():
+    for name, t in zip(_BLOCK_NORM_PARAMS, params):
         if t is not None:
             _tensor(t, name, (dim,), _F32, dev)
+
+
+_BLOCK_NORM_PARAMS = ("scale", "post_gamma", "post_beta", "pre_gamma", "pre_beta")
+
+
+def _like(t):
+    return None if t is None else torch.empty_like(t)
 
 
 def block_norm_forward(desc: jfa_block_norm, x, block, gate=None, scale=None, post_gamma=None,
                        post_beta=None, pre_gamma=None, pre_beta=None, stream=None):
     """Allocates and returns (y, n) of jfa_block_norm_forward; n is None
     without a pre_norm."""
-    params = dict(scale=scale, post_gamma=post_gamma, post_beta=post_beta, pre_gamma=pre_gamma,
-                  pre_beta=pre_beta)
-    _block_norm_args(desc, x, dict(block=block, gate=gate), params)
+    _block_norm_args(desc, x, (block, gate), (scale, post_gamma, post_beta, pre_gamma, pre_beta))
     with _on(x.device, stream) as s:
         y = torch.empty_like(x)
         n = torch.empty_like(x) if desc.pre_norm != NORM["none"] else None
@@ -701,24 +758,15 @@ def block_norm_backward(desc: jfa_block_norm, x, block, gate=None, scale=None, p
     """Allocates and returns the gradients of jfa_block_norm_backward as a dict
     with the keys x, block, gate, scale, post_gamma, post_beta, pre_gamma and
     pre_beta (None for an input that is None)."""
-    params = dict(scale=scale, post_gamma=post_gamma, post_beta=post_beta, pre_gamma=pre_gamma,
-                  pre_beta=pre_beta)
-    _block_norm_args(desc, x, dict(block=block, gate=gate, dy=dy, dn=dn), params)
+    params = (scale, post_gamma, post_beta, pre_gamma, pre_beta)
+    _block_norm_args(desc, x, (block, gate, dy, dn), params)
     with _on(x.device, stream) as s:
         if ws is None:
             ws = block_norm_workspace(desc, x.device)
         elif ws.device != x.device:
             _invalid(f"ws: device {ws.device}, expected {x.device}")
-        g = {"x": torch.empty_like(x), "block": torch.empty_like(x),
-             "gate": None if gate is None else torch.empty_like(x)}
-        # the parameters' gradients: rows of one small buffer, each on 16 bytes
-        dim = desc.dim
-        sums = torch.empty((len(params), (dim + 3) // 4 * 4), dtype=torch.float32, device=x.device)
-        if dim % 4:
-            sums = sums[:, :dim]
-        g.update({k: None if p is None else r for (k, p), r in zip(params.items(), sums.unbind(0))})
+        g = [torch.empty_like(x), torch.empty_like(x), _like(gate)] + [_like(p) for p in params]
         _check(load().jfa_block_norm_backward(
-            ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), _ptr(scale),
-            _ptr(post_gamma), _ptr(post_beta), _ptr(pre_gamma), _ptr(pre_beta), _ptr(dy), _ptr(dn),
-            *map(_ptr, g.values()), ws.data_ptr(), ws.numel() * ws.element_size(), s))
-    return g
+            ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), *[_ptr(p) for p in params],
+            _ptr(dy), _ptr(dn), *[_ptr(t) for t in g], ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    return dict(zip(("x", "block", "gate") + _BLOCK_NORM_PARAMS, g))

@@ -303,6 +303,14 @@ jfa_status jfa_quantize_mxfp4_dequant(const void* x, jfa_dtype dtype, int64_t ro
                                       int along_rows, uint8_t* codes, uint8_t* scales,
                                       void* dequant, jfa_stream_t stream);
 
+/* Both operands of x in one pass over it: codes / scales as
+ * jfa_quantize_mxfp4 with along_rows = 0, codes_t / scales_t as with 1 (an
+ * output's gradient needs both: along rows for the input's gradient, along
+ * columns for the weight's). */
+jfa_status jfa_quantize_mxfp4_both(const void* x, jfa_dtype dtype, int64_t rows, int64_t cols,
+                                   uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
+                                   uint8_t* scales_t, jfa_stream_t stream);
+
 /* Product of two MXFP4 operands on the tensor cores, fp32 accumulation, one
  * rounding at the end:
  *   out[i][j] = sum_k A[i][k] B[j][k]  (+ bias[j])  (+ out[i][j])

@@ -67,7 +67,7 @@ const char* const kKernelNames[K_COUNT] = {
     "sched_prepare", "sched_rank", "simt_fwd", "simt_bwd_pre", "simt_bwd_dq", "simt_bwd_dkdv",
     "mx_along_d", "mx_along_rows", "tc_fwd", "tc_bwd_pre", "tc_bwd", "tc_dq_finalize",
     "tc_fwd_mxfp8", "tc_bias_prep", "dbias_zero_masked", "norm_quantize_mxfp8", "tc_bwd_sq", "tc_fwd_sq",
-    "mx4_rows", "mx4_cols", "mx4_gemm", "mx4_gemm_pair", "block_norm_fwd", "block_norm_bwd",
+    "mx4_rows", "mx4_cols", "mx4_both", "mx4_gemm", "mx4_gemm_pair", "block_norm_fwd", "block_norm_bwd",
     "block_norm_sum"};
 
 }  // namespace

@@ -185,6 +185,7 @@ enum KernelId {
     K_TC_FWD_SQ,
     K_MX4_ROWS,
     K_MX4_COLS,
+    K_MX4_BOTH,
     K_MX4_GEMM,
     K_MX4_GEMM_PAIR,
     K_BLOCK_NORM_FWD,

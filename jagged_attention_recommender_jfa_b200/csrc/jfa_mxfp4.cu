@@ -40,6 +40,8 @@ struct Raw8<__nv_bfloat16> {
         const uint32_t m = absmax_bf16x2(absmax_bf16x2(r.x, r.y), absmax_bf16x2(r.z, r.w));
         return max(m << 16, m & 0xFFFF0000u);   // bits of magnitudes order like the magnitudes
     }
+    // to the shared tile of mx4_both
+    __device__ __forceinline__ void put(uint8_t* s, int row, int lane) const;
     __device__ __forceinline__ void get(float (&f)[8]) const {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -56,6 +58,7 @@ struct Raw8<float> {
         a = __ldg(reinterpret_cast<const float4*>(p));
         b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
+    __device__ __forceinline__ void put(uint8_t* s, int row, int lane) const;
     __device__ __forceinline__ void get(float (&f)[8]) const {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
@@ -306,6 +309,26 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_rows_any(const T
 constexpr int kTile = 128;
 constexpr int kStagePitch = 80;   // bytes per column: 64 of codes, padded to spread the banks
 
+// The staged codes ([column][64 bytes]) and scales ([column][block]) of a tile
+// to the operand of the transpose.
+__device__ __forceinline__ void store_col_tile(const uint8_t* s_codes, const uint8_t* s_scale, int64_t rt, int ct, int cols,
+                                               int64_t blocks_k, int64_t tiles_k, uint8_t* codes, uint8_t* scales) {
+    __syncthreads();
+    // 16 bytes of codes per step: four consecutive threads write a column's 64
+    for (int i = threadIdx.x; i < kTile * 4; i += blockDim.x) {
+        const int col = i >> 2, part = i & 3;
+        if (ct * kTile + col < cols && rt * 4 + part < blocks_k)
+            *reinterpret_cast<uint4*>(codes + ((int64_t)(ct * kTile + col) * blocks_k + rt * 4 + part) * 16) =
+                *reinterpret_cast<const uint4*>(s_codes + col * kStagePitch + part * 16);
+    }
+    // the scale tile: word w holds column (w % 4) * 32 + w / 4
+    if (threadIdx.x < kTile) {
+        const int w = threadIdx.x;
+        const uint32_t word = *reinterpret_cast<const uint32_t*>(s_scale + ((w & 3) * 32 + (w >> 2)) * 4);
+        *reinterpret_cast<uint32_t*>(scales + ((int64_t)ct * tiles_k + rt) * 512 + w * 4) = word;
+    }
+}
+
 template <typename T, int CPT>
 struct Cols;
 template <>
@@ -313,10 +336,11 @@ struct Cols<__nv_bfloat16, 2> {
     uint32_t raw = 0;
     __device__ void load(const __nv_bfloat16* p) { raw = __ldg(reinterpret_cast<const unsigned int*>(p)); }
     __device__ float get(int i) const { return __uint_as_float(i ? (raw & 0xFFFF0000u) : (raw << 16)); }
-    __device__ static void max_bits(const Cols (&v)[32], uint32_t (&m)[2]) {
+    template <int R>
+    __device__ static void max_bits(const Cols (&v)[R], uint32_t (&m)[2]) {
         uint32_t k = 0;
 #pragma unroll
-        for (int t = 0; t < 32; ++t) k = absmax_bf16x2(k, v[t].raw);
+        for (int t = 0; t < R; ++t) k = absmax_bf16x2(k, v[t].raw);
         m[0] = k << 16;
         m[1] = k & 0xFFFF0000u;
     }
@@ -329,10 +353,11 @@ struct Cols<__nv_bfloat16, 1> {
     uint32_t raw = 0;
     __device__ void load(const __nv_bfloat16* p) { raw = __ldg(reinterpret_cast<const unsigned short*>(p)); }
     __device__ float get(int) const { return __uint_as_float(raw << 16); }
-    __device__ static void max_bits(const Cols (&v)[32], uint32_t (&m)[1]) {
+    template <int R>
+    __device__ static void max_bits(const Cols (&v)[R], uint32_t (&m)[1]) {
         uint32_t k = 0;
 #pragma unroll
-        for (int t = 0; t < 32; ++t) k = absmax_bf16x2(k, v[t].raw);
+        for (int t = 0; t < R; ++t) k = absmax_bf16x2(k, v[t].raw);
         m[0] = k << 16;
     }
     __device__ static void store(__nv_bfloat16* p, float a, float) { *p = __float2bfloat16_rn(a); }
@@ -342,10 +367,11 @@ struct Cols<float, 1> {
     float raw = 0.f;
     __device__ void load(const float* p) { raw = __ldg(p); }
     __device__ float get(int) const { return raw; }
-    __device__ static void max_bits(const Cols (&v)[32], uint32_t (&m)[1]) {
+    template <int R>
+    __device__ static void max_bits(const Cols (&v)[R], uint32_t (&m)[1]) {
         float k = 0.f;
 #pragma unroll
-        for (int t = 0; t < 32; t += 2) k = absmax3(k, v[t].raw, v[t + 1].raw);
+        for (int t = 0; t < R; t += 2) k = absmax3(k, v[t].raw, v[t + 1].raw);
         m[0] = __float_as_uint(k);
     }
     __device__ static void store(float* p, float a, float) { *p = a; }
@@ -362,7 +388,7 @@ __global__ void __launch_bounds__(512 / CPT, kColCtas<CPT, DEQ>) mx4_cols(const 
                                                       uint8_t* __restrict__ codes,
                                                       uint8_t* __restrict__ scales, T* __restrict__ y) {
     __shared__ __align__(16) uint8_t s_codes[kTile * kStagePitch];
-    __shared__ uint8_t s_scale[4 * kTile];   // [column][block]
+    __shared__ __align__(4) uint8_t s_scale[4 * kTile];   // [column][block]
     constexpr int kLanes = kTile / CPT;      // threads across the columns
     const int64_t rt = blockIdx.x / (unsigned)col_tiles;   // row tile = k tile of the operand
     const int ct = (int)(blockIdx.x - rt * col_tiles);
@@ -408,20 +434,100 @@ __global__ void __launch_bounds__(512 / CPT, kColCtas<CPT, DEQ>) mx4_cols(const 
                 if (8 * w + u < n) Cols<T, CPT>::store(p + (int64_t)(8 * w + u) * cols, d0[u], d1[u]);
         }
     }
-    __syncthreads();
-    // 16 bytes of codes per step: four consecutive threads write a column's 64
-    for (int i = threadIdx.x; i < kTile * 4; i += blockDim.x) {
-        const int col = i >> 2, part = i & 3;
-        if (ct * kTile + col < cols && rt * 4 + part < blocks_k)
-            *reinterpret_cast<uint4*>(codes + ((int64_t)(ct * kTile + col) * blocks_k + rt * 4 + part) * 16) =
-                *reinterpret_cast<const uint4*>(s_codes + col * kStagePitch + part * 16);
+    store_col_tile(s_codes, s_scale, rt, ct, cols, blocks_k, tiles_k, codes, scales);
+}
+
+// Both operands of x in one pass over it: rows as mx4_rows_vec, and the tile
+// through shared memory for the columns, as raw elements in 16-byte chunks.
+// Chunk j of row i lies at j ^ (i & 7) ^ (i & 16 ? 4 : 0): a half warp writes a
+// row's chunks, and in bf16 reads two rows 16 apart, without bank conflicts.
+// bf16: a lane takes two columns x 16 rows, two lanes a block; fp32: a column
+// x 32 rows.
+template <typename T>
+constexpr int kBothSmem = kTile * kTile * (int)sizeof(T) + kTile * kStagePitch + 4 * kTile + 512;
+
+template <typename T>
+__device__ __forceinline__ int chunk_at(int i, int j) {
+    return i * (kTile * (int)sizeof(T)) + ((j ^ (i & 7) ^ (i & 16 ? 4 : 0)) << 4);
+}
+
+__device__ __forceinline__ void Raw8<__nv_bfloat16>::put(uint8_t* s, int row, int lane) const {
+    *reinterpret_cast<uint4*>(s + chunk_at<__nv_bfloat16>(row, lane)) = r;
+}
+__device__ __forceinline__ void Raw8<float>::put(uint8_t* s, int row, int lane) const {
+    *reinterpret_cast<float4*>(s + chunk_at<float>(row, 2 * lane)) = a;
+    *reinterpret_cast<float4*>(s + chunk_at<float>(row, 2 * lane + 1)) = b;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_both(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
+                                                                     uint8_t* __restrict__ codes, int code_pitch,
+                                                                     uint8_t* __restrict__ scales, int64_t t_blocks,
+                                                                     int64_t t_tiles, uint8_t* __restrict__ t_codes,
+                                                                     uint8_t* __restrict__ t_scales) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t* const s_x = smem;
+    uint8_t* const s_codes = s_x + kTile * kTile * sizeof(T);
+    uint8_t* const s_scale = s_codes + kTile * kStagePitch;
+    uint8_t* const staged = s_scale + 4 * kTile;
+    const RowTile tile(tiles_k);
+    {
+        const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
+        const int c = tile.kt * 128 + lane * 8;
+        Raw8<T> raw[kSegs];
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+            const int64_t r = tile.r0 + i * kHalves + half;
+            if (r < rows && c < cols) raw[i].load(x + r * cols + c);
+        }
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+            const int row = i * kHalves + half;
+            const int64_t r = tile.r0 + row;
+            raw[i].put(s_x, row, lane);
+            uint32_t m = raw[i].max_bits();
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const int b = scale_byte(m);
+            float f[8];
+            raw[i].get(f);
+            const uint32_t code = b == mx4::kNanScale ? 0u : pack8(f, inv_scale(b));
+            if ((lane & 3) == 0) staged[staged_scale(row, lane >> 2)] = (uint8_t)b;
+            if (r < rows && c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + r * code_pitch + c / 2) = code;
+        }
     }
-    // the scale tile: word w holds column (w % 4) * 32 + w / 4
-    if (threadIdx.x < kTile) {
-        const int w = threadIdx.x;
-        const uint32_t word = *reinterpret_cast<const uint32_t*>(s_scale + ((w & 3) * 32 + (w >> 2)) * 4);
-        *reinterpret_cast<uint32_t*>(scales + ((int64_t)ct * tiles_k + rt) * 512 + w * 4) = word;
+    store_scale_tile(staged, scales);   // and the tile is complete
+    {
+        constexpr int CPT = sizeof(T) == 2 ? 2 : 1, R = 32 / CPT, kCols = 32;   // columns and rows a lane, columns a warp
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int blk = warp & 3, cl = (warp >> 2) * kCols + (CPT == 2 ? (lane & 15) * 2 : lane);
+        const int row0 = blk * 32 + (CPT == 2 ? (lane >> 4) * 16 : 0);
+        Cols<T, CPT> v[R];
+#pragma unroll
+        for (int t = 0; t < R; ++t)
+            v[t].raw = *reinterpret_cast<const decltype(v[t].raw)*>(s_x + chunk_at<T>(row0 + t, cl * (int)sizeof(T) / 16) + cl * sizeof(T) % 16);
+        uint32_t amax[CPT];
+        Cols<T, CPT>::max_bits(v, amax);
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            if (CPT == 2) amax[i] = max(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 16));
+            const int b = scale_byte(amax[i]);
+            const float s = inv_scale(b);
+            uint32_t code[R / 8];
+#pragma unroll
+            for (int w = 0; w < R / 8; ++w) {
+                float f[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) f[u] = v[8 * w + u].get(i);
+                code[w] = b == mx4::kNanScale ? 0u : pack8(f, s);
+            }
+            uint8_t* const to = s_codes + (cl + i) * kStagePitch + row0 / 2;
+#pragma unroll
+            for (int w = 0; w < R / 8; w += 2) *reinterpret_cast<uint2*>(to + 4 * w) = make_uint2(code[w], code[w + 1]);
+            if (CPT == 1 || lane < 16) s_scale[(cl + i) * 4 + blk] = (uint8_t)b;
+        }
     }
+    store_col_tile(s_codes, s_scale, tile.r0 / kTile, tile.kt, cols, t_blocks, t_tiles, t_codes, t_scales);
 }
 
 template <typename T, bool DEQ>
@@ -449,6 +555,22 @@ cudaError_t launch_cols(const T* x, int64_t rows, int cols, uint8_t* codes, uint
     return cudaGetLastError();
 }
 
+// Widths whose rows are not 16-byte aligned take two passes.
+template <typename T>
+cudaError_t launch_both(const T* x, int64_t rows, int cols, uint8_t* codes, uint8_t* scales, uint8_t* t_codes,
+                        uint8_t* t_scales, cudaStream_t st) {
+    const int tiles_k = (int)mx4::scale_tiles_k(cols);
+    const int64_t grid = mx4::scale_tiles_r(rows) * tiles_k;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = cudaFuncSetAttribute(mx4_both<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBothSmem<T>);
+    if (e != cudaSuccess) return e;
+    prof_begin(st);
+    mx4_both<T><<<(unsigned)grid, kRowThreads, kBothSmem<T>, st>>>(x, rows, cols, tiles_k, codes, (int)(mx4::padded_cols(cols) / 2),
+                                                                   scales, (rows + 31) / 32, mx4::scale_tiles_k(rows), t_codes, t_scales);
+    prof_end(st, K_MX4_BOTH);
+    return cudaGetLastError();
+}
+
 // A bf16 row of an even width is 4-byte aligned, so its columns can be taken
 // in pairs; other widths take one column per thread.
 template <bool DEQ>
@@ -467,20 +589,46 @@ cudaError_t dispatch(const void* x, int dtype, int64_t rows, int cols, int along
                          : launch_cols<__nv_bfloat16, 1, DEQ>(p, rows, cols, codes, scales, o, st);
 }
 
-jfa_status quantize_entry(const void* x, int dtype, int64_t rows, int64_t cols, int along_rows, uint8_t* codes,
-                          uint8_t* scales, void* dequant, jfa_stream_t stream) {
+jfa_status check_quantize(const char* who, const void* x, int dtype, int64_t rows, int64_t cols, const uint8_t* codes,
+                          const uint8_t* scales, const void* other, const void* other2) {
     if (dtype != JFA_F32 && dtype != JFA_BF16)
-        return set_last_error(JFA_ERR_INVALID_ARGUMENT, "quantize_mxfp4: dtype must be JFA_F32 or JFA_BF16");
+        return set_last_error(JFA_ERR_INVALID_ARGUMENT, "%s: dtype must be JFA_F32 or JFA_BF16", who);
     if (rows < 0 || cols < 0 || rows > kMx4MaxDim || cols > kMx4MaxDim)
-        return set_last_error(JFA_ERR_INVALID_ARGUMENT, "quantize_mxfp4: rows and cols in [0, 2^30]");
+        return set_last_error(JFA_ERR_INVALID_ARGUMENT, "%s: rows and cols in [0, 2^30]", who);
     if (rows == 0 || cols == 0) return JFA_OK;
-    if (!x || !codes || !scales) return set_last_error(JFA_ERR_INVALID_ARGUMENT, "quantize_mxfp4: NULL tensor");
-    if (((uintptr_t)x | (uintptr_t)codes | (uintptr_t)scales | (uintptr_t)dequant) & 15)
-        return set_last_error(JFA_ERR_INVALID_ARGUMENT, "quantize_mxfp4: tensors must be 16-byte aligned");
+    if (!x || !codes || !scales) return set_last_error(JFA_ERR_INVALID_ARGUMENT, "%s: NULL tensor", who);
+    if (((uintptr_t)x | (uintptr_t)codes | (uintptr_t)scales | (uintptr_t)other | (uintptr_t)other2) & 15)
+        return set_last_error(JFA_ERR_INVALID_ARGUMENT, "%s: tensors must be 16-byte aligned", who);
+    return JFA_OK;
+}
+
+jfa_status quantize_entry(const char* who, const void* x, int dtype, int64_t rows, int64_t cols, int along_rows,
+                          uint8_t* codes, uint8_t* scales, void* dequant, jfa_stream_t stream) {
+    const jfa_status s = check_quantize(who, x, dtype, rows, cols, codes, scales, dequant, nullptr);
+    if (s != JFA_OK || rows == 0 || cols == 0) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = dequant ? dispatch<true>(x, dtype, rows, (int)cols, along_rows, codes, scales, dequant, st)
                                   : dispatch<false>(x, dtype, rows, (int)cols, along_rows, codes, scales, nullptr, st);
-    if (e != cudaSuccess) return set_last_error(JFA_ERR_CUDA, "quantize_mxfp4: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return set_last_error(JFA_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+    return JFA_OK;
+}
+
+jfa_status quantize_both(const char* who, const void* x, int dtype, int64_t rows, int64_t cols, uint8_t* codes,
+                         uint8_t* scales, uint8_t* t_codes, uint8_t* t_scales, jfa_stream_t stream) {
+    const jfa_status s = check_quantize(who, x, dtype, rows, cols, codes, scales, t_codes, t_scales);
+    if (s != JFA_OK || rows == 0 || cols == 0) return s;
+    if (!t_codes || !t_scales) return set_last_error(JFA_ERR_INVALID_ARGUMENT, "%s: NULL tensor", who);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (cols % 8 == 0) {
+        e = dtype == JFA_F32 ? launch_both(reinterpret_cast<const float*>(x), rows, (int)cols, codes, scales, t_codes, t_scales, st)
+                             : launch_both(reinterpret_cast<const __nv_bfloat16*>(x), rows, (int)cols, codes, scales, t_codes,
+                                           t_scales, st);
+    } else {
+        e = dispatch<false>(x, dtype, rows, (int)cols, 0, codes, scales, nullptr, st);
+        if (e == cudaSuccess) e = dispatch<false>(x, dtype, rows, (int)cols, 1, t_codes, t_scales, nullptr, st);
+    }
+    if (e != cudaSuccess) return set_last_error(JFA_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
     return JFA_OK;
 }
 
@@ -501,14 +649,19 @@ size_t jfa_mxfp4_scale_bytes(int64_t rows, int64_t cols) {
 
 jfa_status jfa_quantize_mxfp4(const void* x, jfa_dtype dtype, int64_t rows, int64_t cols, int along_rows,
                               uint8_t* codes, uint8_t* scales, jfa_stream_t stream) {
-    return jfa::quantize_entry(x, dtype, rows, cols, along_rows, codes, scales, nullptr, stream);
+    return jfa::quantize_entry("quantize_mxfp4", x, dtype, rows, cols, along_rows, codes, scales, nullptr, stream);
 }
 
 jfa_status jfa_quantize_mxfp4_dequant(const void* x, jfa_dtype dtype, int64_t rows, int64_t cols, int along_rows,
                                       uint8_t* codes, uint8_t* scales, void* dequant, jfa_stream_t stream) {
     if (rows > 0 && cols > 0 && !dequant)
         return jfa::set_last_error(JFA_ERR_INVALID_ARGUMENT, "quantize_mxfp4_dequant: NULL dequant");
-    return jfa::quantize_entry(x, dtype, rows, cols, along_rows, codes, scales, dequant, stream);
+    return jfa::quantize_entry("quantize_mxfp4_dequant", x, dtype, rows, cols, along_rows, codes, scales, dequant, stream);
+}
+
+jfa_status jfa_quantize_mxfp4_both(const void* x, jfa_dtype dtype, int64_t rows, int64_t cols, uint8_t* codes,
+                                   uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, jfa_stream_t stream) {
+    return jfa::quantize_both("quantize_mxfp4_both", x, dtype, rows, cols, codes, scales, codes_t, scales_t, stream);
 }
 
 }  // extern "C"

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import itertools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -45,6 +46,7 @@ EXPORTS = ("jfa_workspace_bytes", "jfa_forward", "jfa_backward", "jfa_quantize_m
            "jfa_block_offsets", "jfa_test_inject", "jfa_forward_mxfp8",
            "jfa_norm_quantize_mxfp8", "jfa_mxfp4_code_bytes", "jfa_mxfp4_scale_bytes",
            "jfa_mxfp4_workspace_bytes", "jfa_quantize_mxfp4", "jfa_quantize_mxfp4_dequant",
+           "jfa_quantize_mxfp4_both",
            "jfa_matmul_mxfp4", "jfa_block_norm_workspace_bytes", "jfa_block_norm_forward",
            "jfa_block_norm_backward")
 NORM = {"none": 0, "rms": 1, "layer": 2}
@@ -141,6 +143,8 @@ def load():
         lib.jfa_quantize_mxfp4.restype = i32
         lib.jfa_quantize_mxfp4_dequant.argtypes = [P, i32, i64, i64, i32, P, P, P, P]
         lib.jfa_quantize_mxfp4_dequant.restype = i32
+        lib.jfa_quantize_mxfp4_both.argtypes = [P, i32, i64, i64, P, P, P, P, P]
+        lib.jfa_quantize_mxfp4_both.restype = i32
         lib.jfa_matmul_mxfp4.argtypes = [i64, i64, i64, P, P, P, P, P, P, i32, i32, P, sz, P]
         lib.jfa_matmul_mxfp4.restype = i32
         PN = ctypes.POINTER(jfa_block_norm)
@@ -353,6 +357,12 @@ def jfa_quantize_mxfp4_dequant(x, dtype, rows, cols, along_rows, codes, scales, 
     _check(load().jfa_quantize_mxfp4_dequant(_addr(x), DTYPE.get(dtype, dtype), int(rows),
                                              int(cols), int(bool(along_rows)), _addr(codes),
                                              _addr(scales), _addr(dequant), _stream(stream)))
+
+
+def jfa_quantize_mxfp4_both(x, dtype, rows, cols, codes, scales, codes_t, scales_t, stream=None):
+    _check(load().jfa_quantize_mxfp4_both(_addr(x), DTYPE.get(dtype, dtype), int(rows), int(cols),
+                                          _addr(codes), _addr(scales), _addr(codes_t),
+                                          _addr(scales_t), _stream(stream)))
 
 
 def jfa_matmul_mxfp4(m, n, k, a_codes, a_scales, b_codes, b_scales, bias, out, out_dtype,
@@ -587,6 +597,18 @@ def quantize_mxfp4(x, along_rows=False, want_dequant=False, stream=None):
         return MxOperand(codes, scales, r, c)
 
 
+def quantize_mxfp4_both(x, stream=None):
+    """The MXFP4 operands of ``x`` and of its transpose, in one pass."""
+    rows, cols = _matrix(x)
+    u8 = torch.uint8
+    with _on(x.device, stream) as s:
+        ops = tuple(MxOperand(x.new_empty((r, _code_pitch(c)), dtype=u8), x.new_empty(_scale_bytes(r, c), dtype=u8), r, c)
+                    for r, c in ((rows, cols), (cols, rows)))
+        _check(load().jfa_quantize_mxfp4_both(x.data_ptr(), _TORCH_DTYPE[x.dtype], rows, cols,
+                                              *[t.data_ptr() for o in ops for t in o[:2]], s))
+    return ops
+
+
 def _operand(o, name, device=None):
     if not isinstance(o, MxOperand):
         _invalid(f"{name}: an MxOperand is needed")
@@ -605,11 +627,10 @@ def _ws_on(ws, device):
     return ws
 
 
-def _product(m, n, k, a, a_scales, b: MxOperand, bias, out, accumulate, ws, s):
-    """jfa_matmul_mxfp4 on checked arguments; a and a_scales are addresses."""
+def _product(m, n, k, a, a_scales, b, b_scales, bias, out, accumulate, ws, s):
+    """jfa_matmul_mxfp4 on checked arguments; the operands are addresses."""
     _check(load().jfa_matmul_mxfp4(
-        m, n, k, a, a_scales, b.codes.data_ptr(), b.scales.data_ptr(), _ptr(bias), out.data_ptr(),
-        _TORCH_DTYPE[out.dtype], 1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), s))
+        m, n, k, a, a_scales, b, b_scales, _ptr(bias), out.data_ptr(), _TORCH_DTYPE[out.dtype], 1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), s))
 
 
 def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torch.bfloat16,
@@ -636,7 +657,8 @@ def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torc
         ws = _ws_on(ws, dev)
         if out is None:
             out = a.codes.new_empty((m, n), dtype=out_dtype)
-        _product(m, n, k, a.codes.data_ptr(), a.scales.data_ptr(), b, bias, out, accumulate, ws, s)
+        _product(m, n, k, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(), bias,
+                 out, accumulate, ws, s)
         if check:
             jfa_check_error(ws, s)
     return out
@@ -661,7 +683,7 @@ def linear_mxfp4_forward(x, w: MxOperand, bias=None, ws=None, stream=None, check
         _check(load().jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 0, codes,
                                          codes + code_bytes, s))
         out = x.new_empty((m, n))
-        _product(m, n, k, codes, codes + code_bytes, w, bias, out, False, ws, s)
+        _product(m, n, k, codes, codes + code_bytes, w.codes.data_ptr(), w.scales.data_ptr(), bias, out, False, ws, s)
         if check:
             jfa_check_error(ws, s)
     return out
@@ -685,24 +707,21 @@ def linear_mxfp4_backward(dy, x, w_t: MxOperand, dw=None, ws=None, stream=None, 
     if accumulate:
         _tensor(dw, "dw", (n, k), _F32, dev)
     dt = _TORCH_DTYPE[dy.dtype]
-    row_codes, col_codes, pitch = m * _code_pitch(n), n * _code_pitch(m), _code_pitch(m)
+    # one buffer: the codes and scales of dy, of its transpose and of x's
+    sizes = [m * _code_pitch(n), _scale_bytes(m, n), n * _code_pitch(m), _scale_bytes(n, m), k * _code_pitch(m),
+             _scale_bytes(k, m)]
     with _on(dev, stream) as s:
         ws = _ws_on(ws, dev)
         lib = load()
-        # one buffer: dy's operand, then (behind the first product) its transpose's
-        buf = dy.new_empty(max(row_codes + _scale_bytes(m, n), col_codes + _scale_bytes(n, m)), dtype=torch.uint8)
-        p = buf.data_ptr()
-        _check(lib.jfa_quantize_mxfp4(dy.data_ptr(), dt, m, n, 0, p, p + row_codes, s))
+        buf = dy.new_empty(sum(sizes), dtype=torch.uint8)
+        a, a_s, t, t_s, b, b_s = itertools.accumulate([buf.data_ptr()] + sizes[:-1])
+        _check(lib.jfa_quantize_mxfp4_both(dy.data_ptr(), dt, m, n, a, a_s, t, t_s, s))
         dx = dy.new_empty((m, k))
-        _product(m, k, n, p, p + row_codes, w_t, None, dx, False, ws, s)
-        _check(lib.jfa_quantize_mxfp4(dy.data_ptr(), dt, m, n, 1, p, p + col_codes, s))
-        codes = x.new_empty((k, pitch), dtype=torch.uint8)
-        scales = x.new_empty(_scale_bytes(k, m), dtype=torch.uint8)
-        _check(lib.jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 1, codes.data_ptr(),
-                                      scales.data_ptr(), s))
+        _product(m, k, n, a, a_s, w_t.codes.data_ptr(), w_t.scales.data_ptr(), None, dx, False, ws, s)
+        _check(lib.jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 1, b, b_s, s))
         if not accumulate:
             dw = dy.new_empty((n, k), dtype=torch.float32)
-        _product(n, k, m, p, p + col_codes, MxOperand(codes, scales, k, m), None, dw, accumulate, ws, s)
+        _product(n, k, m, t, t_s, b, b_s, None, dw, accumulate, ws, s)
         if check:
             jfa_check_error(ws, s)
     return dx, dw

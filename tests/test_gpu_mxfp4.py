@@ -62,6 +62,16 @@ def test_quantise_matches_oracle(cuda_device, rows, cols, along_rows, dtype):
     assert torch.equal(plain.codes, op.codes) and torch.equal(plain.scales, op.scales)
 
 
+@pytest.mark.parametrize("rows,cols", SIZES + [(128, 128), (1000, 520)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantise_both_ways_in_one_pass(cuda_device, rows, cols, dtype):
+    x = draw(rows, cols, dtype, rows * 5 + cols)
+    x[0, 0] = float("nan")   # one bad block each way
+    op, op_t = jfa.quantize_mxfp4_both(x.to(cuda_device))
+    check_operand(op, x, False)
+    check_operand(op_t, x, True)
+
+
 @pytest.mark.parametrize("along_rows", [False, True])
 @pytest.mark.parametrize("cols", [256, 131])
 def test_quantise_special_values(cuda_device, along_rows, cols):

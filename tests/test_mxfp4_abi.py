@@ -46,11 +46,19 @@ def test_quantiser_refusals(change, status, dequant):
         refused(status, jfa.jfa_quantize_mxfp4, **a, stream=0)
 
 
+@pytest.mark.parametrize("change", [dict(dtype=2), dict(rows=-1), dict(cols=(1 << 30) + 1), dict(x=None), dict(codes=None),
+                                    dict(scales_t=None), dict(codes_t=None), dict(codes_t=FAKE + 8), dict(x=FAKE + 2)])
+def test_two_way_quantiser_refusals(change):
+    a = dict(x=FAKE, dtype="bf16", rows=10, cols=64, codes=FAKE, scales=FAKE, codes_t=FAKE, scales_t=FAKE)
+    refused(INVALID, jfa.jfa_quantize_mxfp4_both, **{**a, **change}, stream=0)
+
+
 def test_quantiser_dequant_pointer_and_empty():
     refused(INVALID, jfa.jfa_quantize_mxfp4_dequant, FAKE, "f32", 3, 3, 0, FAKE, FAKE, None, stream=0)
     refused(INVALID, jfa.jfa_quantize_mxfp4_dequant, FAKE, "f32", 3, 3, 1, FAKE, FAKE, FAKE + 4, stream=0)
     jfa.jfa_quantize_mxfp4(None, "bf16", 0, 64, 0, None, None, stream=0)
     jfa.jfa_quantize_mxfp4(None, "bf16", 64, 0, 1, None, None, stream=0)
+    jfa.jfa_quantize_mxfp4_both(None, "bf16", 0, 64, None, None, None, None, stream=0)
 
 
 @pytest.mark.parametrize("change,status", [

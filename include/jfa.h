@@ -318,7 +318,7 @@ jfa_status jfa_quantize_mxfp4_both(const void* x, jfa_dtype dtype, int64_t rows,
  * weight [n][k] as a linear layer keeps it); bias: device fp32 [n] or NULL;
  * out: device [m][n], out_dtype JFA_F32 or JFA_BF16, 16-byte aligned, must not
  * overlap the operands; accumulate != 0 adds to what out holds (gradient
- * accumulation).  The gradients of a linear layer y = x w^T are products of
+ * accumulation; an fp32 sum below 2^-126 may come out as zero).  The gradients of a linear layer y = x w^T are products of
  * the same kind: dx = dy w (operands dy along rows, w with along_rows = 1),
  * dw = dy^T x (both with along_rows = 1).  The order of the sums depends only
  * on the sizes: equal calls give equal bits.

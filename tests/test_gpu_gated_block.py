@@ -192,3 +192,33 @@ def test_block_in_a_graph(cuda_device):
         for name in ("x", "block", "gate", "scale", "post_gamma", "pre_gamma"):
             assert torch.equal(g["norm"][name], wg["norm"][name]), name
     jfa.jfa_check_error(ws)
+
+
+def test_streams_side_by_side(cuda_device):
+    # products (their kernels take whole SMs and all of their tensor memory),
+    # norms and the attention on three streams at once, a stream given by its
+    # handle among them
+    dev = cuda_device
+    b, t = Block(dev, 7), Batch(dev, [300] * 12, 8)
+    ws, aws, _, nws = workspaces(t, dev)
+    r = forward(b, t, ws, aws)
+    big = jfa.quantize_mxfp4(torch.randn(6000, 1024, generator=torch.Generator().manual_seed(1)).to(dev))
+    w = jfa.quantize_mxfp4(torch.randn(2048, 1024, generator=torch.Generator().manual_seed(2)).to(dev))
+    heads = lambda z: z.view(t.rows, H, HD)
+    attend = lambda **kw: jfa.attention_forward(t.prob, heads(r["q"]), heads(r["k"]), heads(r["v"]), t.off, t.off, b.table,
+                                                "softmax", True, ws=aws, check=False, **kw)[0]
+    norm = lambda **kw: jfa.block_norm_backward(t.desc, r["x"], r["o"].view(t.rows, D), r["u"], b.scale, b.post_gamma,
+                                                pre_gamma=b.pre_gamma, dy=t.dy, dn=t.dy, ws=nws, **kw)
+    product = lambda **kw: jfa.matmul_mxfp4(big, w, ws=ws, check=False, **kw)
+    want = product(), norm(), attend()
+    streams = [torch.cuda.Stream(dev) for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got.append((product(stream=streams[0]), norm(stream=streams[1].cuda_stream), attend(stream=streams[2])))
+    torch.cuda.synchronize()
+    for p, n, o in got:
+        assert torch.equal(p, want[0]) and torch.equal(o, want[2])
+        assert all(torch.equal(n[k], want[1][k]) for k in n if n[k] is not None)
+    assert torch.equal(jfa.matmul_mxfp4(big, w, ws=ws, stream=0), want[0])
+    jfa.jfa_check_error(aws)

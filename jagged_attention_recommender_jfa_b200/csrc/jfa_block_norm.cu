@@ -229,10 +229,10 @@ struct Cols {
     }
 };
 
-// A thread's parameters, K vectors of P pairs.  With one vector per thread and
-// tensor (MEM) they wait in shared memory, each thread its own: registers are
-// what limits the warps of an SM there, and those hide the latencies of the
-// row sums.  Wider rows keep them in registers.
+// A thread's parameters, K vectors of P pairs.  With up to eight elements per
+// thread and tensor (MEM) they wait in shared memory, each thread its own:
+// registers are what limits the warps of an SM there, and those hide the
+// latencies of the row sums.  Wider rows keep them in registers.
 template <int K, int P, bool MEM>
 struct Params {
     float2 v[K][P];
@@ -383,13 +383,17 @@ __device__ __forceinline__ float to_y(const Par& par, int W1, int W0, int post, 
     return r;
 }
 
-// Registers per thread through the launch bound: 80 for the forward (64 fp32)
+template <typename T, int NCH>
+constexpr bool kParamsInSmem = NCH * Vec<T>::N <= 8;
+
+// Registers per thread through the launch bound: 80 for the forward (64 fp32,
+// 96 with two vectors)
 // and 80 for the fp32 backward with one vector per thread, 128 otherwise.
 // 60000 x 1024 fp32 backward at 128 / 96 / 80 / 64 registers: 451 / 383 / 331 /
 // 350 us; 222283 x 1024 bf16 backward at 128 / 96 / 80: 769 / 1228 / 1670 us
 // (spills), forward at 80 / 64: 393 / 431 us.
 template <typename T, int NCH>
-constexpr int kFwdBound = NCH > 1 ? kMaxThreads : (sizeof(T) == 4 ? 1024 : 768);
+constexpr int kFwdBound = NCH > 1 ? (sizeof(T) == 4 && NCH == 2 ? 640 : kMaxThreads) : (sizeof(T) == 4 ? 1024 : 768);
 template <typename T, int NCH>
 constexpr int kBwdBound = NCH == 1 && sizeof(T) == 4 ? 768 : kMaxThreads;
 
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(kFwdBound<T, NCH>) block_norm_fwd(const NormAr
     extern __shared__ float4 smem4[];
     __shared__ GroupBuf buf;
     Group g(G, &buf);
-    Params<LN ? 4 : 2, P, NCH == 1> par(reinterpret_cast<float*>(smem4));
+    Params<LN ? 4 : 2, P, kParamsInSmem<T, NCH>> par(reinterpret_cast<float*>(smem4));
     const int groups = blockDim.x / G;
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t base = (int64_t)blockIdx.x * groups, row = base + threadIdx.x / G;
@@ -497,8 +501,8 @@ __global__ void __launch_bounds__(kBwdBound<T, NCH>) block_norm_bwd(const NormAr
     float* const smem = reinterpret_cast<float*>(smem4);
     __shared__ GroupBuf buf;
     Group g(G, &buf);
-    Params<kBwdParams<LN>, P, NCH == 1> par(smem);
-    Sums<P, Q, kSmem> sums(smem + (NCH == 1 ? kBwdParams<LN> * 2 * P * blockDim.x : 0));
+    Params<kBwdParams<LN>, P, kParamsInSmem<T, NCH>> par(smem);
+    Sums<P, Q, kSmem> sums(smem + (kParamsInSmem<T, NCH> ? kBwdParams<LN> * 2 * P * blockDim.x : 0));
     const int groups = blockDim.x / G;
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t base = (int64_t)blockIdx.x * groups, row = base + threadIdx.x / G;
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(kBwdBound<T, NCH>) block_norm_bwd(const NormAr
     } else {
         // the groups' sums in group order, through shared memory [groups][D]
         // behind the parameters and sums
-        float* const area = smem + ((NCH == 1 ? kBwdParams<LN> : 0) + (kSmem ? Q : 0)) * 2 * P * blockDim.x;
+        float* const area = smem + ((kParamsInSmem<T, NCH> ? kBwdParams<LN> : 0) + (kSmem ? Q : 0)) * 2 * P * blockDim.x;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             __syncthreads();
@@ -678,9 +682,14 @@ __global__ void __launch_bounds__(32 * kStrands) block_norm_sum(const NormArgs a
     }
 }
 
-// How a row width is cut up: vectors per thread and threads per
-// row, one vector of a row each, a power of two within a warp, whole warps
-// above.  Widths that are no multiple of a vector need one more vector.
+// How a row width is cut up: vectors per thread and threads per row, a power
+// of two within a warp, whole warps above.  Widths that are no multiple of a
+// vector need one more vector.  In fp32 a vector is four elements, and two of
+// them per thread halve the row sums' share of the work: LayerNorm 60000 x
+// 1024 with one / two: forward 258 / 196 us, backward 505 / 410, 100000 x 300
+// backward 307 / 333; RMS 60000 x 1024 forward 187 / 209, backward 336 / 324,
+// 30000 x 2048 (where one per thread leaves one CTA on an SM) backward 437 /
+// 342.  In bf16 one vector of eight is best up to 512 threads.
 struct RowShape {
     int G, threads, nch, groups;
     int period;   // rows after which the alignment repeats
@@ -692,12 +701,13 @@ constexpr int kMostChunks = sizeof(T) == 4 ? 5 : 3;
 static_assert(kMostChunks<float> * kMaxThreads * 4 >= kMaxDim + 4 && kMostChunks<__nv_bfloat16> * kMaxThreads * 8 >= kMaxDim + 8,
               "the widest rows fit");
 
-template <typename T>
+template <typename T, bool LN>
 RowShape row_shape(int D) {
     constexpr int V = Vec<T>::N;
     RowShape s{};
     const int vecs = D % V == 0 ? D / V : (D + V - 2) / V + 1;
-    s.nch = vecs <= kMaxThreads ? 1 : (vecs <= 2 * kMaxThreads ? 2 : kMostChunks<T>);
+    const int one = sizeof(T) == 2 ? kMaxThreads : (LN ? 128 : 384);   // most vectors of a row with one per thread
+    s.nch = vecs <= one ? 1 : (vecs <= 2 * kMaxThreads ? 2 : kMostChunks<T>);
     const int need = (vecs + s.nch - 1) / s.nch;
     if (need > 32) {
         s.G = (need + 31) / 32 * 32;
@@ -772,11 +782,12 @@ cudaError_t allow_smem(K kern, size_t smem) {
 
 template <typename T, bool LN>
 cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
-    const RowShape s = row_shape<T>(a.D);
+    const RowShape s = row_shape<T, LN>(a.D);
     void (*kern)(NormArgs, int) = s.nch == 1   ? block_norm_fwd<T, 1, LN>
                                   : s.nch == 2 ? block_norm_fwd<T, 2, LN>
                                                : block_norm_fwd<T, kMostChunks<T>, LN>;
-    const size_t smem = s.nch == 1 ? Params<LN ? 4 : 2, Vec<T>::N / 2, true>::bytes(s.threads) : 0;
+    const bool in_smem_par = s.nch == 1 || (s.nch == 2 && kParamsInSmem<T, 2>);
+    const size_t smem = in_smem_par ? s.nch * Params<LN ? 4 : 2, Vec<T>::N / 2, true>::bytes(s.threads) : 0;
     int grid = 0;
     cudaError_t e = allow_smem(kern, smem);
     if (e == cudaSuccess) e = row_grid(kern, s, a.rows, smem, 0x7fffffff, &grid);
@@ -790,14 +801,15 @@ cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
 // Returns the number of partial rows in *parts.
 template <typename T, bool LN>
 cudaError_t bwd_launch(const NormArgs& a, int* parts, cudaStream_t st) {
-    const RowShape s = row_shape<T>(a.D);
+    const RowShape s = row_shape<T, LN>(a.D);
     constexpr int Q = LN ? 4 : 2;
     void (*kern)(NormArgs, int) = s.nch == 1   ? block_norm_bwd<T, 1, LN>
                                   : s.nch == 2 ? block_norm_bwd<T, 2, LN>
                                                : block_norm_bwd<T, kMostChunks<T>, LN>;
     const int pairs = s.nch * Vec<T>::N / 2;
+    const bool in_smem_par = s.nch == 1 || (s.nch == 2 && kParamsInSmem<T, 2>);
     const bool in_smem = s.nch == 1 ? kSumsInSmem<T, 1, LN> : (s.nch == 2 ? kSumsInSmem<T, 2, LN> : true);
-    const size_t smem = sizeof(float2) * pairs * s.threads * ((s.nch == 1 ? kBwdParams<LN> : 0) + (in_smem ? Q : 0)) +
+    const size_t smem = sizeof(float2) * pairs * s.threads * ((in_smem_par ? kBwdParams<LN> : 0) + (in_smem ? Q : 0)) +
                         (s.groups > 1 ? sizeof(float) * s.groups * a.D : 0);
     cudaError_t e = allow_smem(kern, smem);
     if (e == cudaSuccess) e = row_grid(kern, s, a.rows, smem, kMaxParts, parts);

@@ -7,7 +7,9 @@ stays within L 2^-24 magnitude.  The chain of a row's result: a sum over up
 to 8192 elements is 16 additions in a thread, 5 shuffles and up to 32 warps,
 two of those in a row per norm (mean, variance), two norms and one sum on the
 way back: 5 x 53 + about 60 elementwise operations (the exponential and the
-fast reciprocal count 4 each) < 340.  Summed over rows: a CTA's rows one
+fast reciprocal count 4 each) < 340.  (Rows of an odd width above 8176 bf16 or
+4096 fp32 columns put up to 24 elements in a thread, but then at most 16 warps
+and four sums in a row: less.)  Summed over rows: a CTA's rows one
 after the other, then partial rows in strands of eight: at most rows / grid +
 grid / 8 + 8 < 200 more for these sizes.  A bf16 result adds half a step, 2^-8
 of the value.

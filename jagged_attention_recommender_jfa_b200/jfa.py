@@ -495,12 +495,17 @@ def attention_backward(problem, q, k, v, out, lse, dout, q_offsets, kv_offsets, 
 # Around the attention: MXFP4 operands and products, block norms.  These take
 # contiguous tensors, run on the tensors' own device and, unless ``stream``
 # says otherwise, on that device's current stream; with ``stream`` the results
-# are allocated on it too.
+# are allocated on it too.  Their small calls are launches of a few
+# microseconds, so the way to them is kept short: arguments are looked over by
+# one expression each, and only a call that fails it is taken apart for its
+# message.
 # ---------------------------------------------------------------------------
 
 _TORCH_DTYPE = {torch.float32: JFA_F32, torch.bfloat16: JFA_BF16}
-_F32, _U8 = (torch.float32,), (torch.uint8,)
-# the current stream's handle by device index, without building a Stream object
+_JFA_DTYPE = {v: k for k, v in _TORCH_DTYPE.items()}
+_U8 = torch.uint8
+# the current device, and its current stream's handle without a Stream object
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -513,59 +518,57 @@ def _invalid(msg: str):
     raise JfaError(JFA_ERR_INVALID_ARGUMENT, msg)
 
 
-def _tensor(t, name, shape, dtypes, device):
-    """A contiguous CUDA tensor of the shape, one of the dtypes and on the device, or an error.
-    (Messages are only built for an error: these checks run before every small launch.)"""
+def _is(t, shape, dtype, index):
+    """Whether t is a contiguous tensor of the shape and dtype on that GPU."""
+    return (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.get_device() == index and t.is_contiguous())
+
+
+def _refuse(t, name, shape, dtypes, index=None):
+    """Says what is wrong with an argument (nothing happens if it is right)."""
     if not isinstance(t, torch.Tensor):
         _invalid(f"{name}: a torch tensor is needed")
-    if t.shape != shape:
+    if t.shape != tuple(shape):
         _invalid(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype not in dtypes:
-        _invalid(f"{name}: dtype {t.dtype} is not one of {dtypes}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        _invalid(f"{name}: device {t.device}, expected {device or 'cuda'}")
+        _invalid(f"{name}: dtype {t.dtype} is not one of {tuple(dtypes)}")
+    if not t.is_cuda or (index is not None and t.get_device() != index):
+        _invalid(f"{name}: device {t.device}, expected {'cuda' if index is None else f'cuda:{index}'}")
     if not t.is_contiguous():
         _invalid(f"{name}: must be contiguous")
 
 
-class _on:
-    """Makes the tensors' device current, and ``stream`` (default: the device's
-    current one) the stream that results are allocated on; enters as its handle."""
-    __slots__ = ("device", "stream", "stack")
+def _matrix(x, name="x"):
+    """Rows and columns of a contiguous bf16 or fp32 matrix on a GPU."""
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_cuda and x.dtype in _TORCH_DTYPE
+            and x.is_contiguous()):
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            _invalid(f"{name}: a 2-D torch tensor is needed")
+        _refuse(x, name, x.shape, _TORCH_DTYPE)
+    return x.shape
 
-    def __init__(self, device, stream):
-        self.device, self.stream, self.stack = device, stream, None
 
-    def __enter__(self):
-        dev, s = self.device, self.stream
-        if s is None and torch.cuda.current_device() == dev.index:
-            return _raw_stream(dev.index)
-        if s is not None and not isinstance(s, torch.cuda.Stream):
-            s = torch.cuda.ExternalStream(int(s), device=dev)
-        if s is not None and s.device != dev:
-            _invalid(f"stream of {s.device} for tensors of {dev}")
-        self.stack = contextlib.ExitStack()
-        self.stack.enter_context(torch.cuda.device(dev))
-        if s is not None:
-            self.stack.enter_context(torch.cuda.stream(s))
-        return torch.cuda.current_stream(dev).cuda_stream
+def _stream_here(index, stream):
+    """The handle of the stream to use as things stand, or None where the
+    device or the current stream has to be switched first (:func:`_switch`)."""
+    return _raw_stream(index) if stream is None and _device() == index else None
 
-    def __exit__(self, *exc):
-        if self.stack is not None:
-            self.stack.__exit__(*exc)
-        return False
+
+@contextlib.contextmanager
+def _switch(device, stream):
+    """Makes ``device`` and, where given, ``stream`` (a Stream or a handle) the
+    current ones."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream is not None and stream.device != device:
+        _invalid(f"stream of {stream.device} for tensors of {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
 
 
 def mxfp4_workspace(device) -> torch.Tensor:
     """The zeroed workspace of :func:`matmul_mxfp4` (an error word; may be shared)."""
-    return torch.zeros(jfa_mxfp4_workspace_bytes(), dtype=torch.uint8, device=device)
-
-
-def _matrix(x, name="x"):
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        _invalid(f"{name}: a 2-D torch tensor is needed")
-    _tensor(x, name, x.shape, _TORCH_DTYPE, None)
-    return x.shape
+    return torch.zeros(jfa_mxfp4_workspace_bytes(), dtype=_U8, device=device)
 
 
 def _code_pitch(cols):
@@ -581,56 +584,82 @@ def quantize_mxfp4(x, along_rows=False, want_dequant=False, stream=None):
     with ``along_rows`` (blocks of 32 rows).  With ``want_dequant`` also
     returns the values it stands for, laid out like ``x``."""
     rows, cols = _matrix(x)
+    s = _stream_here(x.get_device(), stream)
+    if s is None:
+        with _switch(x.device, stream):
+            return quantize_mxfp4(x, along_rows, want_dequant)
     r, c = (cols, rows) if along_rows else (rows, cols)
-    dt, u8 = _TORCH_DTYPE[x.dtype], torch.uint8
-    with _on(x.device, stream) as s:
-        codes = x.new_empty((r, _code_pitch(c)), dtype=u8)
-        scales = x.new_empty(_scale_bytes(r, c), dtype=u8)
-        if want_dequant:
-            dequant = torch.empty_like(x)
-            _check(load().jfa_quantize_mxfp4_dequant(
-                x.data_ptr(), dt, rows, cols, 1 if along_rows else 0, codes.data_ptr(),
-                scales.data_ptr(), dequant.data_ptr(), s))
-            return MxOperand(codes, scales, r, c), dequant
-        _check(load().jfa_quantize_mxfp4(x.data_ptr(), dt, rows, cols, 1 if along_rows else 0,
-                                         codes.data_ptr(), scales.data_ptr(), s))
-        return MxOperand(codes, scales, r, c)
+    dev = x.device
+    codes = torch.empty(r, _code_pitch(c), dtype=_U8, device=dev)
+    scales = torch.empty(_scale_bytes(r, c), dtype=_U8, device=dev)
+    lib = _LIB or load()
+    if want_dequant:
+        dequant = torch.empty_like(x)
+        st = lib.jfa_quantize_mxfp4_dequant(
+            x.data_ptr(), _TORCH_DTYPE[x.dtype], rows, cols, 1 if along_rows else 0,
+            codes.data_ptr(), scales.data_ptr(), dequant.data_ptr(), s)
+        if st:
+            _check(st)
+        return MxOperand(codes, scales, r, c), dequant
+    st = lib.jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], rows, cols,
+                                1 if along_rows else 0, codes.data_ptr(), scales.data_ptr(), s)
+    if st:
+        _check(st)
+    return MxOperand(codes, scales, r, c)
 
 
 def quantize_mxfp4_both(x, stream=None):
     """The MXFP4 operands of ``x`` and of its transpose, in one pass."""
     rows, cols = _matrix(x)
-    u8 = torch.uint8
-    with _on(x.device, stream) as s:
-        ops = tuple(MxOperand(x.new_empty((r, _code_pitch(c)), dtype=u8), x.new_empty(_scale_bytes(r, c), dtype=u8), r, c)
-                    for r, c in ((rows, cols), (cols, rows)))
-        _check(load().jfa_quantize_mxfp4_both(x.data_ptr(), _TORCH_DTYPE[x.dtype], rows, cols,
-                                              *[t.data_ptr() for o in ops for t in o[:2]], s))
+    s = _stream_here(x.get_device(), stream)
+    if s is None:
+        with _switch(x.device, stream):
+            return quantize_mxfp4_both(x)
+    ops = tuple(MxOperand(torch.empty(r, _code_pitch(c), dtype=_U8, device=x.device),
+                          torch.empty(_scale_bytes(r, c), dtype=_U8, device=x.device), r, c)
+                for r, c in ((rows, cols), (cols, rows)))
+    _check(load().jfa_quantize_mxfp4_both(x.data_ptr(), _TORCH_DTYPE[x.dtype], rows, cols,
+                                          *[t.data_ptr() for o in ops for t in o[:2]], s))
     return ops
 
 
-def _operand(o, name, device=None):
+def _operand(o, name, index=None):
+    """The operand's parts; on that GPU, or (index None) on any."""
     if not isinstance(o, MxOperand):
         _invalid(f"{name}: an MxOperand is needed")
-    if o.rows < 0 or o.cols < 0:
-        _invalid(f"{name}: negative size")
-    _tensor(o.codes, name + ".codes", (o.rows, _code_pitch(o.cols)), _U8, device)
-    _tensor(o.scales, name + ".scales", (_scale_bytes(o.rows, o.cols),), _U8, o.codes.device)
+    codes, scales, rows, cols = o
+    if index is None and isinstance(codes, torch.Tensor):
+        index = codes.get_device()
+    if not (rows >= 0 and cols >= 0 and _is(codes, (rows, _code_pitch(cols)), _U8, index)
+            and _is(scales, (_scale_bytes(rows, cols),), _U8, index) and index >= 0):
+        if rows < 0 or cols < 0:
+            _invalid(f"{name}: negative size")
+        _refuse(codes, name + ".codes", (rows, _code_pitch(cols)), (_U8,), index)
+        _refuse(scales, name + ".scales", (_scale_bytes(rows, cols),), (_U8,), index)
+    return o
 
 
-def _ws_on(ws, device):
-    """The caller's workspace, on the device, or a fresh one."""
+def _vector(t, name, n, index):
+    if t is not None and not _is(t, (n,), torch.float32, index):
+        _refuse(t, name, (n,), (torch.float32,), index)
+
+
+def _ws_on(ws, index):
+    """The caller's workspace, on the GPU, or a fresh one."""
     if ws is None:
-        return mxfp4_workspace(device)
-    if ws.device != device:
-        _invalid(f"ws: device {ws.device}, expected {device}")
+        return mxfp4_workspace(torch.device("cuda", index))
+    if ws.get_device() != index:
+        _invalid(f"ws: device {ws.device}, expected cuda:{index}")
     return ws
 
 
 def _product(m, n, k, a, a_scales, b, b_scales, bias, out, accumulate, ws, s):
     """jfa_matmul_mxfp4 on checked arguments; the operands are addresses."""
-    _check(load().jfa_matmul_mxfp4(
-        m, n, k, a, a_scales, b, b_scales, _ptr(bias), out.data_ptr(), _TORCH_DTYPE[out.dtype], 1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    st = (_LIB or load()).jfa_matmul_mxfp4(
+        m, n, k, a, a_scales, b, b_scales, _ptr(bias), out.data_ptr(), _TORCH_DTYPE[out.dtype],
+        1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), s)
+    if st:
+        _check(st)
 
 
 def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torch.bfloat16,
@@ -639,28 +668,30 @@ def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torc
     allocated in ``out_dtype`` unless ``out`` is given; ``accumulate`` adds to
     ``out``.  ``ws``: :func:`mxfp4_workspace`; ``check`` as in
     :func:`attention_forward`."""
-    _operand(a, "a")
-    dev = a.codes.device
-    _operand(b, "b", dev)
-    m, n, k = a.rows, b.rows, a.cols
-    if k != b.cols:
-        _invalid(f"a has {k} columns, b {b.cols}")
-    if bias is not None:
-        _tensor(bias, "bias", (n,), _F32, dev)
+    a_codes, a_scales, m, k = _operand(a, "a")
+    index = a_codes.get_device()
+    b_codes, b_scales, n, kb = _operand(b, "b", index)
+    if k != kb:
+        _invalid(f"a has {k} columns, b {kb}")
+    _vector(bias, "bias", n, index)
     if out is not None:
-        _tensor(out, "out", (m, n), _TORCH_DTYPE, dev)
+        if not (_is(out, (m, n), torch.bfloat16, index) or _is(out, (m, n), torch.float32, index)):
+            _refuse(out, "out", (m, n), _TORCH_DTYPE, index)
     elif accumulate:
         _invalid("accumulate needs out")
     elif out_dtype not in _TORCH_DTYPE:
         _invalid(f"out_dtype {out_dtype} is not one of {tuple(_TORCH_DTYPE)}")
-    with _on(dev, stream) as s:
-        ws = _ws_on(ws, dev)
-        if out is None:
-            out = a.codes.new_empty((m, n), dtype=out_dtype)
-        _product(m, n, k, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(), bias,
-                 out, accumulate, ws, s)
-        if check:
-            jfa_check_error(ws, s)
+    s = _stream_here(index, stream)
+    if s is None:
+        with _switch(a_codes.device, stream):
+            return matmul_mxfp4(a, b, bias, out, out_dtype, accumulate, ws, None, check)
+    ws = _ws_on(ws, index)
+    if out is None:
+        out = torch.empty(m, n, dtype=out_dtype, device=a_codes.device)
+    _product(m, n, k, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
+             bias, out, accumulate, ws, s)
+    if check:
+        jfa_check_error(ws, s)
     return out
 
 
@@ -668,24 +699,28 @@ def linear_mxfp4_forward(x, w: MxOperand, bias=None, ws=None, stream=None, check
     """``x`` [m, k] (quantised here) times the transpose of the weight operand
     ``w`` [n, k] (``quantize_mxfp4`` of the weight), in the dtype of ``x``."""
     m, k = _matrix(x)
-    dev = x.device
-    _operand(w, "w", dev)
-    n = w.rows
-    if k != w.cols:
-        _invalid(f"x has {k} columns, w {w.cols}")
-    if bias is not None:
-        _tensor(bias, "bias", (n,), _F32, dev)
+    index = x.get_device()
+    w_codes, w_scales, n, kw = _operand(w, "w", index)
+    if k != kw:
+        _invalid(f"x has {k} columns, w {kw}")
+    _vector(bias, "bias", n, index)
+    s = _stream_here(index, stream)
+    if s is None:
+        with _switch(x.device, stream):
+            return linear_mxfp4_forward(x, w, bias, ws, None, check)
+    ws = _ws_on(ws, index)
     code_bytes = m * _code_pitch(k)
-    with _on(dev, stream) as s:
-        ws = _ws_on(ws, dev)
-        buf = x.new_empty(code_bytes + _scale_bytes(m, k), dtype=torch.uint8)   # codes, then scales
-        codes = buf.data_ptr()
-        _check(load().jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 0, codes,
-                                         codes + code_bytes, s))
-        out = x.new_empty((m, n))
-        _product(m, n, k, codes, codes + code_bytes, w.codes.data_ptr(), w.scales.data_ptr(), bias, out, False, ws, s)
-        if check:
-            jfa_check_error(ws, s)
+    buf = torch.empty(code_bytes + _scale_bytes(m, k), dtype=_U8, device=x.device)   # codes, then scales
+    codes = buf.data_ptr()
+    st = (_LIB or load()).jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 0, codes,
+                                             codes + code_bytes, s)
+    if st:
+        _check(st)
+    out = torch.empty(m, n, dtype=x.dtype, device=x.device)
+    _product(m, n, k, codes, codes + code_bytes, w_codes.data_ptr(), w_scales.data_ptr(), bias, out,
+             False, ws, s)
+    if check:
+        jfa_check_error(ws, s)
     return out
 
 
@@ -696,34 +731,36 @@ def linear_mxfp4_backward(dy, x, w_t: MxOperand, dw=None, ws=None, stream=None, 
     passed straight through).  ``w_t``: ``quantize_mxfp4(weight,
     along_rows=True)``.  The bias's gradient is ``dy.sum(0)``."""
     m, n = _matrix(dy, "dy")
-    _matrix(x)
-    dev, k = dy.device, x.shape[1]
-    if x.shape[0] != m or x.device != dev:
-        _invalid(f"x: {tuple(x.shape)} on {x.device} does not go with dy: {tuple(dy.shape)} on {dev}")
-    _operand(w_t, "w_t", dev)
-    if w_t.rows != k or w_t.cols != n:
-        _invalid(f"w_t is {w_t.rows} x {w_t.cols}, expected {k} x {n}")
+    mx, k = _matrix(x)
+    index = dy.get_device()
+    if mx != m or x.get_device() != index:
+        _invalid(f"x: {tuple(x.shape)} on {x.device} does not go with dy: {tuple(dy.shape)} on {dy.device}")
+    w_codes, w_scales, kw, nw = _operand(w_t, "w_t", index)
+    if kw != k or nw != n:
+        _invalid(f"w_t is {kw} x {nw}, expected {k} x {n}")
     accumulate = dw is not None
-    if accumulate:
-        _tensor(dw, "dw", (n, k), _F32, dev)
-    dt = _TORCH_DTYPE[dy.dtype]
+    if accumulate and not _is(dw, (n, k), torch.float32, index):
+        _refuse(dw, "dw", (n, k), (torch.float32,), index)
+    s = _stream_here(index, stream)
+    if s is None:
+        with _switch(dy.device, stream):
+            return linear_mxfp4_backward(dy, x, w_t, dw, ws, None, check)
+    ws = _ws_on(ws, index)
+    lib, dev = load(), dy.device
     # one buffer: the codes and scales of dy, of its transpose and of x's
     sizes = [m * _code_pitch(n), _scale_bytes(m, n), n * _code_pitch(m), _scale_bytes(n, m), k * _code_pitch(m),
              _scale_bytes(k, m)]
-    with _on(dev, stream) as s:
-        ws = _ws_on(ws, dev)
-        lib = load()
-        buf = dy.new_empty(sum(sizes), dtype=torch.uint8)
-        a, a_s, t, t_s, b, b_s = itertools.accumulate([buf.data_ptr()] + sizes[:-1])
-        _check(lib.jfa_quantize_mxfp4_both(dy.data_ptr(), dt, m, n, a, a_s, t, t_s, s))
-        dx = dy.new_empty((m, k))
-        _product(m, k, n, a, a_s, w_t.codes.data_ptr(), w_t.scales.data_ptr(), None, dx, False, ws, s)
-        _check(lib.jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 1, b, b_s, s))
-        if not accumulate:
-            dw = dy.new_empty((n, k), dtype=torch.float32)
-        _product(n, k, m, t, t_s, b, b_s, None, dw, accumulate, ws, s)
-        if check:
-            jfa_check_error(ws, s)
+    buf = torch.empty(sum(sizes), dtype=_U8, device=dev)
+    a, a_s, t, t_s, b, b_s = itertools.accumulate([buf.data_ptr()] + sizes[:-1])
+    _check(lib.jfa_quantize_mxfp4_both(dy.data_ptr(), _TORCH_DTYPE[dy.dtype], m, n, a, a_s, t, t_s, s))
+    dx = torch.empty(m, k, dtype=dy.dtype, device=dev)
+    _product(m, k, n, a, a_s, w_codes.data_ptr(), w_scales.data_ptr(), None, dx, False, ws, s)
+    _check(lib.jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 1, b, b_s, s))
+    if not accumulate:
+        dw = torch.empty(n, k, dtype=torch.float32, device=dev)
+    _product(n, k, m, t, t_s, b, b_s, None, dw, accumulate, ws, s)
+    if check:
+        jfa_check_error(ws, s)
     return dx, dw
 
 
@@ -731,25 +768,25 @@ def block_norm_workspace(desc: jfa_block_norm, device) -> torch.Tensor:
     n = jfa_block_norm_workspace_bytes(desc)
     if n == 0:
         raise JfaError(JFA_ERR_INVALID_ARGUMENT, load().jfa_last_error().decode())
-    return torch.empty(n, dtype=torch.uint8, device=device)
-
-
-def _block_norm_args(desc, x, tensors, params):
-    if not isinstance(x, torch.Tensor):
-        _invalid("x: a torch tensor is needed")
-    dt = (torch.bfloat16,) if desc.dtype == JFA_BF16 else _F32
-    dim, dev = desc.dim, x.device
-    shape = (desc.rows, dim)
-    _tensor(x, "x", shape, dt, None)
-    for name, t in zip(("block", "gate", "dy", "dn"), tensors):
-        if t is not None:
-            _tensor(t, name, shape, dt, dev)
-    for name, t in zip(_BLOCK_NORM_PARAMS, params):
-        if t is not None:
-            _tensor(t, name, (dim,), _F32, dev)
+    return torch.empty(n, dtype=_U8, device=device)
 
 
 _BLOCK_NORM_PARAMS = ("scale", "post_gamma", "post_beta", "pre_gamma", "pre_beta")
+
+
+def _block_norm_args(desc, x, tensors, params):
+    """Looks the tensors ([rows, dim]) and parameters ([dim] fp32) over; the GPU's index."""
+    if not isinstance(x, torch.Tensor):
+        _invalid("x: a torch tensor is needed")
+    dim, index, dt = desc.dim, x.get_device(), _JFA_DTYPE.get(desc.dtype, torch.float32)
+    shape, vec = (desc.rows, dim), (dim,)
+    for name, t in zip(("x", "block", "gate", "dy", "dn"), (x,) + tensors):
+        if t is not None and not (_is(t, shape, dt, index) and index >= 0):
+            _refuse(t, name, shape, (dt,), index)
+    for name, t in zip(_BLOCK_NORM_PARAMS, params):
+        if t is not None and not _is(t, vec, torch.float32, index):
+            _refuse(t, name, vec, (torch.float32,), index)
+    return index
 
 
 def _like(t):
@@ -760,14 +797,18 @@ def block_norm_forward(desc: jfa_block_norm, x, block, gate=None, scale=None, po
                        post_beta=None, pre_gamma=None, pre_beta=None, stream=None):
     """Allocates and returns (y, n) of jfa_block_norm_forward; n is None
     without a pre_norm."""
-    _block_norm_args(desc, x, (block, gate), (scale, post_gamma, post_beta, pre_gamma, pre_beta))
-    with _on(x.device, stream) as s:
-        y = torch.empty_like(x)
-        n = torch.empty_like(x) if desc.pre_norm != NORM["none"] else None
-        _check(load().jfa_block_norm_forward(
-            ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), _ptr(scale),
-            _ptr(post_gamma), _ptr(post_beta), _ptr(pre_gamma), _ptr(pre_beta), y.data_ptr(),
-            _ptr(n), s))
+    params = (scale, post_gamma, post_beta, pre_gamma, pre_beta)
+    s = _stream_here(_block_norm_args(desc, x, (block, gate), params), stream)
+    if s is None:
+        with _switch(x.device, stream):
+            return block_norm_forward(desc, x, block, gate, *params)
+    y = torch.empty_like(x)
+    n = torch.empty_like(x) if desc.pre_norm else None
+    st = (_LIB or load()).jfa_block_norm_forward(
+        ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), _ptr(scale), _ptr(post_gamma),
+        _ptr(post_beta), _ptr(pre_gamma), _ptr(pre_beta), y.data_ptr(), _ptr(n), s)
+    if st:
+        _check(st)
     return y, n
 
 
@@ -778,14 +819,19 @@ def block_norm_backward(desc: jfa_block_norm, x, block, gate=None, scale=None, p
     with the keys x, block, gate, scale, post_gamma, post_beta, pre_gamma and
     pre_beta (None for an input that is None)."""
     params = (scale, post_gamma, post_beta, pre_gamma, pre_beta)
-    _block_norm_args(desc, x, (block, gate, dy, dn), params)
-    with _on(x.device, stream) as s:
-        if ws is None:
-            ws = block_norm_workspace(desc, x.device)
-        elif ws.device != x.device:
-            _invalid(f"ws: device {ws.device}, expected {x.device}")
-        g = [torch.empty_like(x), torch.empty_like(x), _like(gate)] + [_like(p) for p in params]
-        _check(load().jfa_block_norm_backward(
-            ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), *[_ptr(p) for p in params],
-            _ptr(dy), _ptr(dn), *[_ptr(t) for t in g], ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    index = _block_norm_args(desc, x, (block, gate, dy, dn), params)
+    s = _stream_here(index, stream)
+    if s is None:
+        with _switch(x.device, stream):
+            return block_norm_backward(desc, x, block, gate, *params, dy=dy, dn=dn, ws=ws)
+    if ws is None:
+        ws = block_norm_workspace(desc, x.device)
+    elif ws.get_device() != index:
+        _invalid(f"ws: device {ws.device}, expected cuda:{index}")
+    g = [torch.empty_like(x), torch.empty_like(x), _like(gate)] + [_like(p) for p in params]
+    st = (_LIB or load()).jfa_block_norm_backward(
+        ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), *[_ptr(p) for p in params],
+        _ptr(dy), _ptr(dn), *[_ptr(t) for t in g], ws.data_ptr(), ws.numel() * ws.element_size(), s)
+    if st:
+        _check(st)
     return dict(zip(("x", "block", "gate") + _BLOCK_NORM_PARAMS, g))

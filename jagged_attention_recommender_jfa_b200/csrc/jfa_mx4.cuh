@@ -55,17 +55,10 @@ __device__ __forceinline__ float scale_value(int byte) {
     return byte > 0 ? __uint_as_float((uint32_t)byte << 23) : __uint_as_float(1u << 22);
 }
 
-// Eight values times s as E2M1 codes, four bits each, value 0 lowest: round to
+// Eight scaled values as E2M1 codes, four bits each, value 0 lowest: round to
 // nearest even, saturating at 6.
-__device__ __forceinline__ uint32_t pack8(const float (&g)[8], float s) {
+__device__ __forceinline__ uint32_t cvt8(const float (&f)[8]) {
     uint32_t o;
-    float f[8];
-#pragma unroll
-    for (int u = 0; u < 8; u += 2) {
-        const float2 v = sm100::mul2(make_float2(g[u], g[u + 1]), make_float2(s, s));
-        f[u] = v.x;
-        f[u + 1] = v.y;
-    }
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
@@ -75,6 +68,32 @@ __device__ __forceinline__ uint32_t pack8(const float (&g)[8], float s) {
         : "=r"(o)
         : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
     return o;
+}
+// Eight values times s as codes.
+__device__ __forceinline__ uint32_t pack8(const float (&g)[8], float s) {
+    float f[8];
+#pragma unroll
+    for (int u = 0; u < 8; u += 2) {
+        const float2 v = sm100::mul2(make_float2(g[u], g[u + 1]), make_float2(s, s));
+        f[u] = v.x;
+        f[u + 1] = v.y;
+    }
+    return cvt8(f);
+}
+// The same from packed bf16: one instruction widens and scales an element
+// (exactly: a power of two; -0 added keeps the sign of a zero).  2^-X of a
+// finite block is a normal bf16 number too.
+__device__ __forceinline__ uint32_t inv_scale_bf16x2(int byte0, int byte1) {
+    return ((uint32_t)(254 - min(byte0, 253)) << 7) | ((uint32_t)(254 - min(byte1, 253)) << 23);
+}
+__device__ __forceinline__ void scaled(uint32_t pair, uint32_t s, float& lo, float& hi) {
+    asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "mov.b32 {c, d}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, a, c, %4;\n\t"
+        "fma.rn.f32.bf16 %1, b, d, %4;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(pair), "r"(s), "f"(-0.0f));
 }
 // The eight values of codes, times s (exact).
 __device__ __forceinline__ void unpack8(uint32_t codes, float s, float (&f)[8]) {

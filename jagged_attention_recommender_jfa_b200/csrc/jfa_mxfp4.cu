@@ -21,35 +21,44 @@ namespace {
 
 using mx4::absmax3;
 using mx4::absmax_bf16x2;
+using mx4::cvt8;
 using mx4::inv_scale;
 using mx4::pack8;
 using mx4::scale_byte;
 using mx4::scale_value;
+using mx4::scaled;
 using mx4::unpack8;
 
-// Eight consecutive elements as they lie in memory; as floats; and the bits of
-// their largest magnitude as an fp32 number (infinities and NaN compare above
-// every finite number, so an exponent field of 255 survives the maximum).
+// Eight consecutive elements as they lie in memory; the bits of their largest
+// magnitude as an fp32 number (infinities and NaN compare above every finite
+// number, so an exponent field of 255 survives the maximum); their codes under
+// a scale byte; and, for rows that end inside them, zeros from element n on.
 template <typename T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
     uint4 r = make_uint4(0u, 0u, 0u, 0u);
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void words(const uint32_t (&w)[4]) { r = make_uint4(w[0], w[1], w[2], w[3]); }
+    __device__ __forceinline__ static uint32_t first(uint32_t w, int n) { return n >= 2 ? w : n == 1 ? w & 0xFFFFu : 0u; }
+    __device__ __forceinline__ void clip(int n) {
+        r = make_uint4(first(r.x, n), first(r.y, n - 2), first(r.z, n - 4), first(r.w, n - 6));
+    }
     __device__ __forceinline__ uint32_t max_bits() const {
         const uint32_t m = absmax_bf16x2(absmax_bf16x2(r.x, r.y), absmax_bf16x2(r.z, r.w));
         return max(m << 16, m & 0xFFFF0000u);   // bits of magnitudes order like the magnitudes
     }
+    __device__ __forceinline__ uint32_t codes(int byte) const {
+        const uint32_t s = mx4::inv_scale_bf16x2(byte, byte);
+        float f[8];
+        scaled(r.x, s, f[0], f[1]);
+        scaled(r.y, s, f[2], f[3]);
+        scaled(r.z, s, f[4], f[5]);
+        scaled(r.w, s, f[6], f[7]);
+        return byte == mx4::kNanScale ? 0u : cvt8(f);
+    }
     // to the shared tile of mx4_both
     __device__ __forceinline__ void put(uint8_t* s, int row, int lane) const;
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            f[2 * u] = __uint_as_float(w[u] << 16);
-            f[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u);
-        }
-    }
 };
 template <>
 struct Raw8<float> {
@@ -58,14 +67,22 @@ struct Raw8<float> {
         a = __ldg(reinterpret_cast<const float4*>(p));
         b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
-    __device__ __forceinline__ void put(uint8_t* s, int row, int lane) const;
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    __device__ __forceinline__ void words(const uint32_t (&w)[8]) {
+        a = make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
+        b = make_float4(__uint_as_float(w[4]), __uint_as_float(w[5]), __uint_as_float(w[6]), __uint_as_float(w[7]));
+    }
+    __device__ __forceinline__ void clip(int n) {
+        a = make_float4(n > 0 ? a.x : 0.f, n > 1 ? a.y : 0.f, n > 2 ? a.z : 0.f, n > 3 ? a.w : 0.f);
+        b = make_float4(n > 4 ? b.x : 0.f, n > 5 ? b.y : 0.f, n > 6 ? b.z : 0.f, n > 7 ? b.w : 0.f);
     }
     __device__ __forceinline__ uint32_t max_bits() const {
         return __float_as_uint(absmax3(absmax3(a.x, a.y, a.z), absmax3(a.w, b.x, b.y), absmax3(b.z, b.w, 0.f)));
     }
+    __device__ __forceinline__ uint32_t codes(int byte) const {
+        const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        return byte == mx4::kNanScale ? 0u : pack8(f, inv_scale(byte));
+    }
+    __device__ __forceinline__ void put(uint8_t* s, int row, int lane) const;
 };
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
     uint4 o;
@@ -105,6 +122,10 @@ struct RowTile {
         kt = (int)(blockIdx.x - rt * (unsigned)tiles_k);
     }
 };
+// Rows of the tensor from the tile's row i on.
+__device__ __forceinline__ int rows_left(const RowTile& tile, int64_t rows, int i) {
+    return (int)(rows - tile.r0 < 128 ? rows - tile.r0 : 128) - i;
+}
 // The scale byte of block j of row i of the tile, staged as it is stored.
 __device__ __forceinline__ int staged_scale(int i, int j) { return (i & 31) * 16 + (i >> 5) * 4 + j; }
 __device__ __forceinline__ void store_scale_tile(const uint8_t* staged, uint8_t* scales) {
@@ -122,29 +143,35 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_rows_vec(const T
     const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
     const RowTile tile(tiles_k);
     const int c = tile.kt * 128 + lane * 8;
+    const int left = rows_left(tile, rows, half);
+    const int in = c < cols ? left : 0, out = c / 2 < code_pitch ? left : 0;   // rows to read, to write codes of
+    const int64_t at = (tile.r0 + half) * cols + c, step = (int64_t)kHalves * cols;
+    const T* p = x + at;
+    T* o = y + at;
+    uint8_t* q = codes + (tile.r0 + half) * code_pitch + c / 2;
     Raw8<T> raw[kSegs];
 #pragma unroll
     for (int i = 0; i < kSegs; ++i) {
-        const int64_t r = tile.r0 + i * kHalves + half;
-        if (r < rows && c < cols) raw[i].load(x + r * cols + c);
+        if (i * kHalves < in) raw[i].load(p);
+        p += step;
     }
 #pragma unroll
     for (int i = 0; i < kSegs; ++i) {
-        const int64_t r = tile.r0 + i * kHalves + half;
         uint32_t m = raw[i].max_bits();
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const int b = scale_byte(m);
-        float f[8];
-        raw[i].get(f);
-        const uint32_t code = b == mx4::kNanScale ? 0u : pack8(f, inv_scale(b));
+        const uint32_t code = raw[i].codes(b);
         if ((lane & 3) == 0) staged[staged_scale(i * kHalves + half, lane >> 2)] = (uint8_t)b;
-        if (r >= rows) continue;
-        if (c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + r * code_pitch + c / 2) = code;
-        if (DEQ && c < cols) {
-            float d[8];
-            unpack8(code, scale_value(b), d);
-            store8(y + r * cols + c, d);
+        if (i * kHalves < out) *reinterpret_cast<uint32_t*>(q) = code;
+        q += (int64_t)kHalves * code_pitch;
+        if (DEQ) {
+            if (i * kHalves < in) {
+                float d[8];
+                unpack8(code, scale_value(b), d);
+                store8(o, d);
+            }
+            o += step;
         }
     }
     store_scale_tile(staged, scales);
@@ -168,14 +195,6 @@ __device__ __forceinline__ void window(const uint32_t (&w)[W + 4], int half, uin
     for (int i = 0; i < W; ++i) o[i] = half & 1 ? __byte_perm(b[i], b[i + 1], 0x5432) : b[i];
 }
 
-template <typename T>
-__device__ __forceinline__ void from_words(const uint32_t (&w)[2 * sizeof(T)], float (&f)[8]) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        if (sizeof(T) == 4) f[u] = __uint_as_float(w[sizeof(T) == 4 ? u : 0]);
-        else f[u] = __uint_as_float(u & 1 ? (w[u / 2] & 0xFFFF0000u) : (w[u / 2] << 16));
-    }
-}
 template <typename T>
 __device__ __forceinline__ void to_words(const float (&f)[8], uint32_t (&w)[2 * sizeof(T)]) {
 #pragma unroll
@@ -246,18 +265,14 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_rows_any(const T
             }
             uint32_t mine[W];
             window<W>(w[i], shift * (int)sizeof(T) / 2, mine);
-            float f[8];
-            from_words<T>(mine, f);
-            if (c + 8 > cols) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (c + u >= cols) f[u] = 0.f;   // the next row's
-            }
-            uint32_t m = __float_as_uint(absmax3(absmax3(f[0], f[1], f[2]), absmax3(f[3], f[4], f[5]), absmax3(f[6], f[7], 0.f)));
+            Raw8<T> e;
+            e.words(mine);
+            if (c + 8 > cols) e.clip(cols - c);   // the rest is the next row's
+            uint32_t m = e.max_bits();
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const int b = scale_byte(m);
-            const uint32_t code = b == mx4::kNanScale ? 0u : pack8(f, inv_scale(b));
+            const uint32_t code = e.codes(b);
             if ((lane & 3) == 0) staged[staged_scale((i0 + i) * kHalves + half, lane >> 2)] = (uint8_t)b;
             if (r < rows && c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + r * code_pitch + c / 2) = code;
             if (DEQ) {
@@ -280,13 +295,13 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_rows_any(const T
                 T* const row = y + r * cols;
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    const int e = c - shift + n * V;
-                    if (e >= tile.kt * 128 && e + V <= lim) {
-                        *reinterpret_cast<uint4*>(row + e) = make_uint4(out[4 * n], out[4 * n + 1], out[4 * n + 2], out[4 * n + 3]);
-                    } else if (e < lim) {
+                    const int at = c - shift + n * V;
+                    if (at >= tile.kt * 128 && at + V <= lim) {
+                        *reinterpret_cast<uint4*>(row + at) = make_uint4(out[4 * n], out[4 * n + 1], out[4 * n + 2], out[4 * n + 3]);
+                    } else if (at < lim) {
 #pragma unroll
                         for (int u = 0; u < V; ++u)
-                            if (e + u >= tile.kt * 128 && e + u < lim) put_element<T, W>(row + e + u, out, n * V + u);
+                            if (at + u >= tile.kt * 128 && at + u < lim) put_element<T, W>(row + at + u, out, n * V + u);
                     }
                 }
                 // the last lane's elements behind its last aligned vector
@@ -329,50 +344,59 @@ __device__ __forceinline__ void store_col_tile(const uint8_t* s_codes, const uin
     }
 }
 
+// A row's elements of a lane's columns; of R rows the scale bytes (PAIRED: of
+// the block's rows that this lane and lane ^ 16 hold) and the codes.
 template <typename T, int CPT>
 struct Cols;
-template <>
-struct Cols<__nv_bfloat16, 2> {
-    uint32_t raw = 0;
-    __device__ void load(const __nv_bfloat16* p) { raw = __ldg(reinterpret_cast<const unsigned int*>(p)); }
-    __device__ float get(int i) const { return __uint_as_float(i ? (raw & 0xFFFF0000u) : (raw << 16)); }
-    template <int R>
-    __device__ static void max_bits(const Cols (&v)[R], uint32_t (&m)[2]) {
+template <int CPT>
+struct Cols<__nv_bfloat16, CPT> {
+    uint32_t raw = 0;   // CPT == 1: in the lower half
+    __device__ void load(const __nv_bfloat16* p) {
+        raw = CPT == 2 ? __ldg(reinterpret_cast<const unsigned int*>(p)) : __ldg(reinterpret_cast<const unsigned short*>(p));
+    }
+    template <int R, bool PAIRED>
+    __device__ static void quantize(const Cols (&v)[R], int (&b)[CPT], uint32_t (&code)[CPT][R / 8]) {
         uint32_t k = 0;
 #pragma unroll
         for (int t = 0; t < R; ++t) k = absmax_bf16x2(k, v[t].raw);
-        m[0] = k << 16;
-        m[1] = k & 0xFFFF0000u;
+        if (PAIRED) k = absmax_bf16x2(k, __shfl_xor_sync(0xffffffffu, k, 16));
+        const int lo = scale_byte(k << 16), hi = scale_byte(k & 0xFFFF0000u);
+        const uint32_t s = mx4::inv_scale_bf16x2(lo, hi);
+        b[0] = lo;
+        b[CPT - 1] = CPT == 2 ? hi : lo;
+#pragma unroll
+        for (int w = 0; w < R / 8; ++w) {
+            float f[8], g[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) scaled(v[8 * w + u].raw, s, f[u], g[u]);
+            code[0][w] = lo == mx4::kNanScale ? 0u : cvt8(f);
+            if (CPT == 2) code[CPT - 1][w] = hi == mx4::kNanScale ? 0u : cvt8(g);
+        }
     }
     __device__ static void store(__nv_bfloat16* p, float a, float b) {
-        *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+        if (CPT == 2) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+        else *p = __float2bfloat16_rn(a);
     }
-};
-template <>
-struct Cols<__nv_bfloat16, 1> {
-    uint32_t raw = 0;
-    __device__ void load(const __nv_bfloat16* p) { raw = __ldg(reinterpret_cast<const unsigned short*>(p)); }
-    __device__ float get(int) const { return __uint_as_float(raw << 16); }
-    template <int R>
-    __device__ static void max_bits(const Cols (&v)[R], uint32_t (&m)[1]) {
-        uint32_t k = 0;
-#pragma unroll
-        for (int t = 0; t < R; ++t) k = absmax_bf16x2(k, v[t].raw);
-        m[0] = k << 16;
-    }
-    __device__ static void store(__nv_bfloat16* p, float a, float) { *p = __float2bfloat16_rn(a); }
 };
 template <>
 struct Cols<float, 1> {
     float raw = 0.f;
     __device__ void load(const float* p) { raw = __ldg(p); }
-    __device__ float get(int) const { return raw; }
-    template <int R>
-    __device__ static void max_bits(const Cols (&v)[R], uint32_t (&m)[1]) {
+    template <int R, bool PAIRED>
+    __device__ static void quantize(const Cols (&v)[R], int (&b)[1], uint32_t (&code)[1][R / 8]) {
+        static_assert(!PAIRED, "a lane holds whole blocks");
         float k = 0.f;
 #pragma unroll
         for (int t = 0; t < R; t += 2) k = absmax3(k, v[t].raw, v[t + 1].raw);
-        m[0] = __float_as_uint(k);
+        b[0] = scale_byte(__float_as_uint(k));
+        const float s = inv_scale(b[0]);
+#pragma unroll
+        for (int w = 0; w < R / 8; ++w) {
+            float f[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) f[u] = v[8 * w + u].raw;
+            code[0][w] = b[0] == mx4::kNanScale ? 0u : pack8(f, s);
+        }
     }
     __device__ static void store(float* p, float a, float) { *p = a; }
 };
@@ -400,23 +424,16 @@ __global__ void __launch_bounds__(512 / CPT, kColCtas<CPT, DEQ>) mx4_cols(const 
     if (c < cols) {
         const T* p = x + r0 * cols + c;
 #pragma unroll
-        for (int t = 0; t < 32; ++t)
-            if (t < n) v[t].load(p + (int64_t)t * cols);
+        for (int t = 0; t < 32; ++t) {
+            if (t < n) v[t].load(p);
+            p += cols;
+        }
     }
-    uint32_t code[CPT][4], amax[CPT];
+    uint32_t code[CPT][4];
     int b[CPT];
-    Cols<T, CPT>::max_bits(v, amax);
+    Cols<T, CPT>::template quantize<32, false>(v, b, code);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-        b[i] = scale_byte(amax[i]);
-        const float s = inv_scale(b[i]);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            float f[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) f[u] = v[8 * w + u].get(i);
-            code[i][w] = b[i] == mx4::kNanScale ? 0u : pack8(f, s);
-        }
         *reinterpret_cast<uint4*>(s_codes + (cl + i) * kStagePitch + blk * 16) =
             make_uint4(code[i][0], code[i][1], code[i][2], code[i][3]);
         s_scale[(cl + i) * 4 + blk] = (uint8_t)b[i];
@@ -430,8 +447,10 @@ __global__ void __launch_bounds__(512 / CPT, kColCtas<CPT, DEQ>) mx4_cols(const 
             unpack8(code[0][w], k0, d0);
             unpack8(code[CPT - 1][w], k1, d1);
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (8 * w + u < n) Cols<T, CPT>::store(p + (int64_t)(8 * w + u) * cols, d0[u], d1[u]);
+            for (int u = 0; u < 8; ++u) {
+                if (8 * w + u < n) Cols<T, CPT>::store(p, d0[u], d1[u]);
+                p += cols;
+            }
         }
     }
     store_col_tile(s_codes, s_scale, rt, ct, cols, blocks_k, tiles_k, codes, scales);
@@ -474,26 +493,28 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_both(const T* __
     {
         const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
         const int c = tile.kt * 128 + lane * 8;
+        const int left = rows_left(tile, rows, half);
+        const int in = c < cols ? left : 0, out = c / 2 < code_pitch ? left : 0;
+        const T* p = x + (tile.r0 + half) * cols + c;
+        uint8_t* q = codes + (tile.r0 + half) * code_pitch + c / 2;
         Raw8<T> raw[kSegs];
 #pragma unroll
         for (int i = 0; i < kSegs; ++i) {
-            const int64_t r = tile.r0 + i * kHalves + half;
-            if (r < rows && c < cols) raw[i].load(x + r * cols + c);
+            if (i * kHalves < in) raw[i].load(p);
+            p += (int64_t)kHalves * cols;
         }
 #pragma unroll
         for (int i = 0; i < kSegs; ++i) {
             const int row = i * kHalves + half;
-            const int64_t r = tile.r0 + row;
             raw[i].put(s_x, row, lane);
             uint32_t m = raw[i].max_bits();
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const int b = scale_byte(m);
-            float f[8];
-            raw[i].get(f);
-            const uint32_t code = b == mx4::kNanScale ? 0u : pack8(f, inv_scale(b));
+            const uint32_t code = raw[i].codes(b);
             if ((lane & 3) == 0) staged[staged_scale(row, lane >> 2)] = (uint8_t)b;
-            if (r < rows && c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + r * code_pitch + c / 2) = code;
+            if (i * kHalves < out) *reinterpret_cast<uint32_t*>(q) = code;
+            q += (int64_t)kHalves * code_pitch;
         }
     }
     store_scale_tile(staged, scales);   // and the tile is complete
@@ -506,25 +527,15 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_both(const T* __
 #pragma unroll
         for (int t = 0; t < R; ++t)
             v[t].raw = *reinterpret_cast<const decltype(v[t].raw)*>(s_x + chunk_at<T>(row0 + t, cl * (int)sizeof(T) / 16) + cl * sizeof(T) % 16);
-        uint32_t amax[CPT];
-        Cols<T, CPT>::max_bits(v, amax);
+        uint32_t code[CPT][R / 8];
+        int b[CPT];
+        Cols<T, CPT>::template quantize<R, CPT == 2>(v, b, code);
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
-            if (CPT == 2) amax[i] = max(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 16));
-            const int b = scale_byte(amax[i]);
-            const float s = inv_scale(b);
-            uint32_t code[R / 8];
-#pragma unroll
-            for (int w = 0; w < R / 8; ++w) {
-                float f[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) f[u] = v[8 * w + u].get(i);
-                code[w] = b == mx4::kNanScale ? 0u : pack8(f, s);
-            }
             uint8_t* const to = s_codes + (cl + i) * kStagePitch + row0 / 2;
 #pragma unroll
-            for (int w = 0; w < R / 8; w += 2) *reinterpret_cast<uint2*>(to + 4 * w) = make_uint2(code[w], code[w + 1]);
-            if (CPT == 1 || lane < 16) s_scale[(cl + i) * 4 + blk] = (uint8_t)b;
+            for (int w = 0; w < R / 8; w += 2) *reinterpret_cast<uint2*>(to + 4 * w) = make_uint2(code[i][w], code[i][w + 1]);
+            if (CPT == 1 || lane < 16) s_scale[(cl + i) * 4 + blk] = (uint8_t)b[i];
         }
     }
     store_col_tile(s_codes, s_scale, tile.r0 / kTile, tile.kt, cols, t_blocks, t_tiles, t_codes, t_scales);

@@ -34,22 +34,25 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// Scale byte of a block from the bits of its largest magnitude:
+// The shared exponent of a block from the bits of its largest magnitude:
 // X = floor(log2(amax)) - 2 (2 = the largest E2M1 exponent) clamped to
-// [-127, 127], byte X + 127.  The biased fp32 exponent e of a normal amax is
-// floor(log2) + 127, so the byte is e - 2, and 0 (X = -127) where that is
-// negative or amax is zero or subnormal.  e = 255: infinity or NaN.
-__device__ __forceinline__ int scale_byte(uint32_t amax_bits) {
-    const int e = (int)(amax_bits >> 23);
-    return e == 255 ? kNanScale : max(e - 2, 0);
-}
-
-// 2^-X and 2^X of a scale byte (X = byte - 127).  Bytes of finite blocks are
-// at most 252, so 2^-X is a normal number (2^-125 .. 2^127); 2^-127 is an
-// fp32 subnormal.
-__device__ __forceinline__ float inv_scale(int byte) {
-    return __uint_as_float((uint32_t)(254 - min(byte, 253)) << 23);
-}
+// [-127, 127].  The biased fp32 exponent e of a normal amax is floor(log2) + 127,
+// so X + 127 is e - 2, and 0 where that is negative or amax is zero or subnormal.
+// e = 255: an infinity or NaN.  x is at most 252 for finite blocks, so 2^-X is a
+// normal number (2^-125 .. 2^127) in fp32 and bf16; it is 2^-126 for the others.
+struct Shared {
+    int x;
+    bool nan;
+    __device__ __forceinline__ explicit Shared(uint32_t amax_bits) {
+        const int e = (int)(amax_bits >> 23);
+        x = max(e - 2, 0);
+        nan = e == 255;
+    }
+    __device__ __forceinline__ int byte() const { return nan ? kNanScale : x; }
+    __device__ __forceinline__ float inv() const { return __uint_as_float((uint32_t)(254 - x) << 23); }
+    __device__ __forceinline__ uint32_t inv_bf16x2() const { return (uint32_t)(254 - x) * 0x00800080u; }
+};
+// The byte X + 127's 2^X; 2^-127 is a subnormal.
 __device__ __forceinline__ float scale_value(int byte) {
     if (byte == kNanScale) return __uint_as_float(0x7FFFFFFFu);
     return byte > 0 ? __uint_as_float((uint32_t)byte << 23) : __uint_as_float(1u << 22);
@@ -80,12 +83,8 @@ __device__ __forceinline__ uint32_t pack8(const float (&g)[8], float s) {
     }
     return cvt8(f);
 }
-// The same from packed bf16: one instruction widens and scales an element
-// (exactly: a power of two; -0 added keeps the sign of a zero).  2^-X of a
-// finite block is a normal bf16 number too.
-__device__ __forceinline__ uint32_t inv_scale_bf16x2(int byte0, int byte1) {
-    return ((uint32_t)(254 - min(byte0, 253)) << 7) | ((uint32_t)(254 - min(byte1, 253)) << 23);
-}
+// A packed pair of bf16 widened and scaled by a packed pair of powers of two
+// (exactly; -0 added keeps the sign of a zero).
 __device__ __forceinline__ void scaled(uint32_t pair, uint32_t s, float& lo, float& hi) {
     asm("{\n\t.reg .b16 a, b, c, d;\n\t"
         "mov.b32 {a, b}, %2;\n\t"
@@ -113,6 +112,27 @@ __device__ __forceinline__ void unpack8(uint32_t codes, float s, float (&f)[8]) 
         f[2 * i] = p.x;
         f[2 * i + 1] = p.y;
     }
+}
+// Of two codes (the lowest byte) the values as packed bf16, times packed scales:
+// shifted by three bits, the fp16 pattern of an E2M1 value is that of the value
+// times 2^-112 in bf16.  Both products are exact.
+__device__ __forceinline__ uint32_t scale_bf16x2(int byte) {
+    return byte == kNanScale ? 0x7FFF7FFFu : byte > 0 ? (uint32_t)byte * 0x00800080u : 0x00400040u;
+}
+__device__ __forceinline__ uint32_t value_bf16x2(uint32_t codes, uint32_t s) {
+    uint32_t h, o;
+    asm("{\n\t.reg .b8 a;\n\t"
+        "cvt.u8.u32 a, %1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+        : "=r"(h)
+        : "r"(codes));
+    h = (h & 0x80008000u) | ((h >> 3) & 0x0FFF0FFFu);
+    asm("{\n\t.reg .b32 t;\n\t"
+        "mul.rn.bf16x2 t, %1, %2;\n\t"
+        "mul.rn.bf16x2 %0, t, %3;\n\t}"
+        : "=r"(o)
+        : "r"(h), "r"(0x77807780u), "r"(s));
+    return o;
 }
 }  // namespace mx4
 }  // namespace jfa

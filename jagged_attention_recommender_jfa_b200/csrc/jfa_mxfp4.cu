@@ -22,17 +22,16 @@ namespace {
 using mx4::absmax3;
 using mx4::absmax_bf16x2;
 using mx4::cvt8;
-using mx4::inv_scale;
 using mx4::pack8;
-using mx4::scale_byte;
 using mx4::scale_value;
 using mx4::scaled;
+using mx4::Shared;
 using mx4::unpack8;
 
 // Eight consecutive elements as they lie in memory; the bits of their largest
 // magnitude as an fp32 number (infinities and NaN compare above every finite
 // number, so an exponent field of 255 survives the maximum); their codes under
-// a scale byte; and, for rows that end inside them, zeros from element n on.
+// a shared exponent; and, for rows that end inside them, zeros from element n on.
 template <typename T>
 struct Raw8;
 template <>
@@ -48,14 +47,14 @@ struct Raw8<__nv_bfloat16> {
         const uint32_t m = absmax_bf16x2(absmax_bf16x2(r.x, r.y), absmax_bf16x2(r.z, r.w));
         return max(m << 16, m & 0xFFFF0000u);   // bits of magnitudes order like the magnitudes
     }
-    __device__ __forceinline__ uint32_t codes(int byte) const {
-        const uint32_t s = mx4::inv_scale_bf16x2(byte, byte);
+    __device__ __forceinline__ uint32_t codes(const Shared& sh) const {
+        const uint32_t s = sh.inv_bf16x2();
         float f[8];
         scaled(r.x, s, f[0], f[1]);
         scaled(r.y, s, f[2], f[3]);
         scaled(r.z, s, f[4], f[5]);
         scaled(r.w, s, f[6], f[7]);
-        return byte == mx4::kNanScale ? 0u : cvt8(f);
+        return sh.nan ? 0u : cvt8(f);
     }
     // to the shared tile of mx4_both
     __device__ __forceinline__ void put(uint8_t* s, int row, int lane) const;
@@ -78,9 +77,9 @@ struct Raw8<float> {
     __device__ __forceinline__ uint32_t max_bits() const {
         return __float_as_uint(absmax3(absmax3(a.x, a.y, a.z), absmax3(a.w, b.x, b.y), absmax3(b.z, b.w, 0.f)));
     }
-    __device__ __forceinline__ uint32_t codes(int byte) const {
+    __device__ __forceinline__ uint32_t codes(const Shared& sh) const {
         const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        return byte == mx4::kNanScale ? 0u : pack8(f, inv_scale(byte));
+        return sh.nan ? 0u : pack8(f, sh.inv());
     }
     __device__ __forceinline__ void put(uint8_t* s, int row, int lane) const;
 };
@@ -102,29 +101,39 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
 // A CTA of the row kernels takes 128 rows x 128 columns: one scale tile, whose
 // 512 bytes leave together (those of rows and blocks behind the tensor as
 // zeros).  Sixteen lanes take a segment (the tile's part of a row), eight
-// elements each; the loads of a half warp's four segments are all in flight
+// elements each; the loads of all of a half warp's segments are in flight
 // before the first conversion.  The first version walked the segments in
 // memory order and stored each scale byte by itself: 12% of its time.
-constexpr int kRowThreads = 512;
-constexpr int kHalves = kRowThreads / 16, kSegs = 128 / kHalves;
-
-// CTAs an SM should hold (registers): 222283 x 1024 bf16 with the copy at 2 / 3 /
-// 4: 179 / 156 / 160 us; fp32 has twice the bytes per thread in flight.
+//
+// Next to HBM these kernels are bound by instructions (75 a warp for its eight
+// elements a lane, 70% of the issue slots at 5.3 TB/s), so a thread takes many
+// segments to share its addresses.  bf16, us, 512 threads and 3 CTAs an SM / 256
+// and 4 / 256 and 5: 65537 x 4096 107 / 103 / 109, both ways 183 / 171 / 205.
+// fp32 (twice the bytes per segment), 512 and 2 / 256 and 2: 65537 x 1003 64 /
+// 68, both ways of 65537 x 1024 70 / 76.
 template <typename T>
-constexpr int kRowCtas = sizeof(T) == 2 ? 3 : 2;
+constexpr int kRowThreads = sizeof(T) == 2 ? 256 : 512;
+template <typename T>
+constexpr int kHalvesOf = kRowThreads<T> / 16;
+template <typename T>
+constexpr int kRowCtas = sizeof(T) == 2 ? 4 : 2;
+// mx4_rows_any, 222283 x 1023 bf16 without / with the copy: 146 / 255 us at 3,
+// 140 / 261 at 4 (spills with the copy).
+template <typename T>
+constexpr int kAnyCtas = sizeof(T) == 2 ? 3 : 2;
 
-struct RowTile {
-    int64_t r0;   // first row
-    int kt;       // column tile
-    __device__ __forceinline__ RowTile(int tiles_k) {
-        const unsigned rt = blockIdx.x / (unsigned)tiles_k;
-        r0 = (int64_t)rt * 128;
-        kt = (int)(blockIdx.x - rt * (unsigned)tiles_k);
+struct Tile {
+    int64_t rt, r0;   // row tile and its first row
+    int kt;           // column tile
+    __device__ __forceinline__ explicit Tile(int tiles_k) {
+        rt = blockIdx.x / (unsigned)tiles_k;
+        r0 = rt * 128;
+        kt = (int)(blockIdx.x - (unsigned)rt * (unsigned)tiles_k);
     }
 };
 // Rows of the tensor from the tile's row i on.
-__device__ __forceinline__ int rows_left(const RowTile& tile, int64_t rows, int i) {
-    return (int)(rows - tile.r0 < 128 ? rows - tile.r0 : 128) - i;
+__device__ __forceinline__ int rows_left(int64_t r0, int64_t rows, int i) {
+    return (int)(rows - r0 < 128 ? rows - r0 : 128) - i;
 }
 // The scale byte of block j of row i of the tile, staged as it is stored.
 __device__ __forceinline__ int staged_scale(int i, int j) { return (i & 31) * 16 + (i >> 5) * 4 + j; }
@@ -136,14 +145,15 @@ __device__ __forceinline__ void store_scale_tile(const uint8_t* staged, uint8_t*
 
 // cols % 8 == 0: a lane's eight elements are 16 or 32 aligned bytes.
 template <typename T, bool DEQ>
-__global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_rows_vec(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
+__global__ void __launch_bounds__(kRowThreads<T>, kRowCtas<T>) mx4_rows_vec(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
                                                                          uint8_t* __restrict__ codes, int code_pitch,
                                                                          uint8_t* __restrict__ scales, T* __restrict__ y) {
+    constexpr int kHalves = kHalvesOf<T>, kSegs = 128 / kHalves;
     __shared__ __align__(16) uint8_t staged[512];
     const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
-    const RowTile tile(tiles_k);
+    const Tile tile(tiles_k);
     const int c = tile.kt * 128 + lane * 8;
-    const int left = rows_left(tile, rows, half);
+    const int left = rows_left(tile.r0, rows, half);
     const int in = c < cols ? left : 0, out = c / 2 < code_pitch ? left : 0;   // rows to read, to write codes of
     const int64_t at = (tile.r0 + half) * cols + c, step = (int64_t)kHalves * cols;
     const T* p = x + at;
@@ -160,8 +170,9 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_rows_vec(const T
         uint32_t m = raw[i].max_bits();
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int b = scale_byte(m);
-        const uint32_t code = raw[i].codes(b);
+        const Shared sh(m);
+        const int b = sh.byte();
+        const uint32_t code = raw[i].codes(sh);
         if ((lane & 3) == 0) staged[staged_scale(i * kHalves + half, lane >> 2)] = (uint8_t)b;
         if (i * kHalves < out) *reinterpret_cast<uint32_t*>(q) = code;
         q += (int64_t)kHalves * code_pitch;
@@ -177,140 +188,238 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_rows_vec(const T
     store_scale_tile(staged, scales);
 }
 
-// Any width.  A segment starts `shift` elements behind a 16-byte boundary; lane
-// l loads the aligned vectors from that boundary on (8 elements' worth), takes
-// the first vector of lane l + 1, and shifts its own eight elements out of the
-// two.  The dequantised copy goes the other way: each lane puts together the
-// aligned vectors that start in its elements' place from its own and the last
-// of lane l - 1, and only the ends of a segment go element by element.
-// The window of W words that starts `half` half words into w.
-template <int W>
-__device__ __forceinline__ void window(const uint32_t (&w)[W + 4], int half, uint32_t (&o)[W]) {
-    uint32_t a[W + 2], b[W + 1];
+// Any width.  A row of the tile starts `shift` elements behind a 16-byte
+// boundary, the same for all rows of a thread (they are a multiple of eight
+// apart).  Lane l takes the aligned vectors from 8 l - shift on and works on
+// them in place: of lanes 0, 4, 8 and 12 the first `shift` elements (lo) belong
+// to the block before, so these lanes have two maxima and two scales.  Only the
+// codes are shifted, by a funnel shift of a lane's and the next lane's.  The
+// last `shift` elements of a tile's row lie in one vector more: those a half
+// warp needs are held by its first lanes and finished together, after the rows.
+// A first version shifted the elements themselves, and the dequantised ones
+// back: 222283 x 1023 bf16 174 us, 340 with the copy, now 146 and 255; 65537 x
+// 1003 fp32 76 and 127, now 64 and 109.  Bound by the ALU pipe (80% busy).
+
+// Which elements of eight are the first n: masks of packed pairs, or n itself.
+template <typename T>
+struct Lo;
+template <>
+struct Lo<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ __forceinline__ explicit Lo(int n) {
 #pragma unroll
-    for (int i = 0; i < W + 2; ++i) a[i] = half & 4 ? w[i + 2] : w[i];
+        for (int k = 0; k < 4; ++k) w[k] = Raw8<__nv_bfloat16>::first(0xFFFFFFFFu, n - 2 * k);
+    }
+    __device__ __forceinline__ uint32_t pick(int k, uint32_t lo, uint32_t hi) const { return (w[k] & lo) | (~w[k] & hi); }
+};
+template <>
+struct Lo<float> {
+    int n;   // below 4
+    __device__ __forceinline__ explicit Lo(int n_) : n(n_) {}
+    __device__ __forceinline__ float pick(int u, float lo, float hi) const { return u < 3 && u < n ? lo : hi; }
+};
+
+__device__ __forceinline__ void max_split(const Raw8<__nv_bfloat16>& e, const Lo<__nv_bfloat16>& l, uint32_t& lo, uint32_t& hi) {
+    const uint32_t x[4] = {e.r.x, e.r.y, e.r.z, e.r.w};
+    uint32_t a[4], b[4];
 #pragma unroll
-    for (int i = 0; i < W + 1; ++i) b[i] = half & 2 ? a[i + 1] : a[i];
-#pragma unroll
-    for (int i = 0; i < W; ++i) o[i] = half & 1 ? __byte_perm(b[i], b[i + 1], 0x5432) : b[i];
+    for (int k = 0; k < 4; ++k) {
+        a[k] = x[k] & l.w[k];
+        b[k] = x[k] & ~l.w[k];
+    }
+    const uint32_t m = absmax_bf16x2(absmax_bf16x2(a[0], a[1]), absmax_bf16x2(a[2], a[3]));
+    const uint32_t n = absmax_bf16x2(absmax_bf16x2(b[0], b[1]), absmax_bf16x2(b[2], b[3]));
+    lo = max(m << 16, m & 0xFFFF0000u);
+    hi = max(n << 16, n & 0xFFFF0000u);
+}
+__device__ __forceinline__ void max_split(const Raw8<float>& e, const Lo<float>& l, uint32_t& lo, uint32_t& hi) {
+    lo = __float_as_uint(absmax3(l.pick(0, e.a.x, 0.f), l.pick(1, e.a.y, 0.f), l.pick(2, e.a.z, 0.f)));
+    hi = __float_as_uint(absmax3(absmax3(l.pick(0, 0.f, e.a.x), l.pick(1, 0.f, e.a.y), l.pick(2, 0.f, e.a.z)),
+                                 absmax3(e.a.w, e.b.x, e.b.y), absmax3(e.b.z, e.b.w, 0.f)));
 }
 
-template <typename T>
-__device__ __forceinline__ void to_words(const float (&f)[8], uint32_t (&w)[2 * sizeof(T)]) {
-#pragma unroll
-    for (int i = 0; i < (int)(2 * sizeof(T)); ++i) {
-        if (sizeof(T) == 4) {
-            w[i] = __float_as_uint(f[i]);
-        } else {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(f[(2 * i) & 7], f[(2 * i + 1) & 7]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&v);
-        }
-    }
+// Eight elements as codes, the lo ones scaled by one power of two (packed bf16;
+// fp32 takes the upper half).
+__device__ __forceinline__ uint32_t split_codes(const Raw8<__nv_bfloat16>& e, const Lo<__nv_bfloat16>& l, uint32_t p, uint32_t q) {
+    float f[8];
+    scaled(e.r.x, l.pick(0, p, q), f[0], f[1]);
+    scaled(e.r.y, l.pick(1, p, q), f[2], f[3]);
+    scaled(e.r.z, l.pick(2, p, q), f[4], f[5]);
+    scaled(e.r.w, l.pick(3, p, q), f[6], f[7]);
+    return cvt8(f);
 }
-// Element u of packed words, as stored.
-template <typename T, int W>
-__device__ __forceinline__ void put_element(T* p, const uint32_t (&w)[W], int u) {
-    if (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(p) = w[sizeof(T) == 4 ? u : 0];
-    else *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[sizeof(T) == 4 ? 0 : u / 2] >> (16 * (u & 1)));
+__device__ __forceinline__ uint32_t split_codes(const Raw8<float>& e, const Lo<float>& l, uint32_t p2, uint32_t q2) {
+    const float p = __uint_as_float(p2 & 0xFFFF0000u), q = __uint_as_float(q2 & 0xFFFF0000u);
+    const float f[8] = {e.a.x * l.pick(0, p, q), e.a.y * l.pick(1, p, q), e.a.z * l.pick(2, p, q), e.a.w * q,
+                        e.b.x * q, e.b.y * q, e.b.z * q, e.b.w * q};
+    return cvt8(f);
+}
+
+// The values of eight codes as they are stored.
+__device__ __forceinline__ void split_values(uint32_t code, const Lo<__nv_bfloat16>& l, int b_lo, int b_hi, uint32_t (&w)[4]) {
+    const uint32_t p = mx4::scale_bf16x2(b_lo), q = mx4::scale_bf16x2(b_hi);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = mx4::value_bf16x2(code >> (8 * k), l.pick(k, p, q));
+}
+__device__ __forceinline__ void split_values(uint32_t code, const Lo<float>& l, int b_lo, int b_hi, uint32_t (&w)[8]) {
+    const float p = scale_value(b_lo), q = scale_value(b_hi);
+    float f[8];
+    unpack8(code, 1.f, f);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) w[u] = __float_as_uint(f[u] * l.pick(u, p, q));
+}
+
+// The half words of an aligned vector (four words) from s on, and before s, in
+// at most three stores.
+__device__ __forceinline__ void store_from(uint16_t* p, const uint32_t* w, int s) {
+    if (s & 1) p[s] = (uint16_t)((s & 4 ? (s & 2 ? w[3] : w[2]) : (s & 2 ? w[1] : w[0])) >> 16);
+    const int a = (s + 1) >> 1;   // first whole word
+    if (a & 1) reinterpret_cast<uint32_t*>(p)[a] = a & 2 ? w[3] : w[1];
+    if (a > 0 && a < 3) reinterpret_cast<uint2*>(p)[1] = make_uint2(w[2], w[3]);
+}
+__device__ __forceinline__ void store_before(uint16_t* p, const uint32_t* w, int s) {
+    if (s & 4) reinterpret_cast<uint2*>(p)[0] = make_uint2(w[0], w[1]);
+    if (s & 2) reinterpret_cast<uint32_t*>(p)[s & 4 ? 2 : 0] = s & 4 ? w[2] : w[0];
+    if (s & 1) p[s - 1] = (uint16_t)(s & 4 ? (s & 2 ? w[3] : w[2]) : (s & 2 ? w[1] : w[0]));
 }
 
 template <typename T, bool DEQ>
-__global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_rows_any(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
+__global__ void __launch_bounds__(kRowThreads<T>, kAnyCtas<T>) mx4_rows_any(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
                                                                          uint8_t* __restrict__ codes, int code_pitch,
                                                                          uint8_t* __restrict__ scales, T* __restrict__ y) {
-    constexpr int V = 16 / sizeof(T), N = 8 / V, W = 4 * N;   // elements of a vector, vectors and words of eight elements
-    constexpr int kBatch = 2;                                 // segments under way at a time
+    constexpr int kHalves = kHalvesOf<T>, kSegs = 128 / kHalves;
+    constexpr int V = 16 / sizeof(T), N = 8 / V, H = sizeof(T) / 2;   // elements of a vector, vectors of eight, half words
     __shared__ __align__(16) uint8_t staged[512];
     const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
-    const int64_t total = rows * cols;
-    const RowTile tile(tiles_k);
-    const int c = tile.kt * 128 + lane * 8;
-#pragma unroll 1
-    for (int i0 = 0; i0 < kSegs; i0 += kBatch) {
-        uint32_t w[kBatch][W + 4];
+    const Tile tile(tiles_k);
+    const int left = rows_left(tile.r0, rows, half);
+    const int c0 = tile.kt * 128, lim = min(cols, c0 + 128);
+    const int64_t row = (tile.r0 + half) * cols, step = (int64_t)kHalves * cols;
+    const int shift = (int)(row & (V - 1)), c = c0 + lane * 8 - shift;   // the lane's first column
+    const T* const end = x + rows * cols;
+    const T* p = x + row + c;
+    // eight elements' worth of vectors, or one vector
+    auto load = [&](Raw8<T>& e, const T* from, int col, bool one) {
+        uint32_t w[4 * N];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int64_t r = tile.r0 + (i0 + i) * kHalves + half;
-            const int shift = (int)((r * cols) % V), first = c - shift;   // column of the lane's first vector
-            const int64_t off = r * cols + first;
-#pragma unroll
-            for (int n = 0; n <= N; ++n) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                const int64_t at = off + n * V;
-                // the last lane also needs the vector behind its own
-                if (r < rows && first + n * V < cols && (n < N || lane == 15)) {
-                    if (at + V <= total) {
-                        v = __ldg(reinterpret_cast<const uint4*>(x + at));
-                    } else {
-                        T* e = reinterpret_cast<T*>(&v);   // the tensor ends inside this vector
-#pragma unroll
-                        for (int u = 0; u < V; ++u)
-                            if (at + u < total) e[u] = x[at + u];
-                    }
-                }
-                w[i][4 * n] = v.x;
-                w[i][4 * n + 1] = v.y;
-                w[i][4 * n + 2] = v.z;
-                w[i][4 * n + 3] = v.w;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int64_t r = tile.r0 + (i0 + i) * kHalves + half;
-            const int shift = (int)((r * cols) % V);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t next = __shfl_down_sync(0xffffffffu, w[i][k], 1, 16);
-                if (lane < 15) w[i][W + k] = next;
-            }
-            uint32_t mine[W];
-            window<W>(w[i], shift * (int)sizeof(T) / 2, mine);
-            Raw8<T> e;
-            e.words(mine);
-            if (c + 8 > cols) e.clip(cols - c);   // the rest is the next row's
-            uint32_t m = e.max_bits();
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const int b = scale_byte(m);
-            const uint32_t code = e.codes(b);
-            if ((lane & 3) == 0) staged[staged_scale((i0 + i) * kHalves + half, lane >> 2)] = (uint8_t)b;
-            if (r < rows && c / 2 < code_pitch) *reinterpret_cast<uint32_t*>(codes + r * code_pitch + c / 2) = code;
-            if (DEQ) {
-                float d[8];
-                unpack8(code, scale_value(b), d);
-                uint32_t both[W + 4], out[W];   // the last vector of lane - 1, then this lane's
-                to_words<T>(d, mine);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) both[k] = __shfl_up_sync(0xffffffffu, mine[W - 4 + k], 1, 16);
-#pragma unroll
-                for (int k = 0; k < W; ++k) both[4 + k] = mine[k];
-                if (shift == 0) {
-#pragma unroll
-                    for (int k = 0; k < W; ++k) out[k] = mine[k];
+        for (int n = 0; n < N; ++n) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if ((n == 0 || !one) && col + n * V < cols) {
+                if (from + (n + 1) * V <= end) {
+                    v = __ldg(reinterpret_cast<const uint4*>(from + n * V));
                 } else {
-                    window<W>(both, 8 - shift * (int)sizeof(T) / 2, out);
+                    T* t = reinterpret_cast<T*>(&v);   // the tensor ends inside this vector
+#pragma unroll
+                    for (int u = 0; u < V; ++u)
+                        if (from + n * V + u < end) t[u] = from[n * V + u];
                 }
-                if (r >= rows) continue;
-                const int lim = min(cols, tile.kt * 128 + 128);
-                T* const row = y + r * cols;
+            }
+            w[4 * n] = v.x;
+            w[4 * n + 1] = v.y;
+            w[4 * n + 2] = v.z;
+            w[4 * n + 3] = v.w;
+        }
+        e.words(w);
+    };
+    Raw8<T> raw[kSegs], ext;
+    if (tile.r0 + 128 + 8 <= rows) {   // eight rows more are at least a vector
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+            uint32_t w[4 * N] = {};
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                if (c + n * V < cols) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + n * V));
+                    w[4 * n] = v.x;
+                    w[4 * n + 1] = v.y;
+                    w[4 * n + 2] = v.z;
+                    w[4 * n + 3] = v.w;
+                }
+            raw[i].words(w);
+            p += step;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+            if (i * kHalves < left) load(raw[i], p, c, false);
+            p += step;
+        }
+    }
+    // lane i < kSegs: the vector behind row i's last lane
+    const int ext_col = c0 + 128 - shift, ext_n = min(max(cols - ext_col, 0), shift);
+    if (lane < kSegs && lane * kHalves < left && ext_n > 0) load(ext, x + row + lane * step + ext_col, ext_col, true);
+    ext.clip(ext_n);
+    const uint32_t ext_max = ext.max_bits();
+
+    const int lo_n = lane & 3 ? 0 : shift;
+    const Lo<T> lo(lo_n);
+    const uint32_t lo_codes = (1u << (4 * lo_n)) - 1u;
+    uint8_t* q = codes + (tile.r0 + half) * code_pitch + c0 / 2 + lane * 4;
+    const int out = c0 + lane * 8 < 2 * code_pitch ? left : 0;
+    T* o = y + row + c;
+    uint32_t ext_m = 0u, ext_code = 0u;
+#pragma unroll
+    for (int i = 0; i < kSegs; ++i) {
+        if (c + 8 > cols) raw[i].clip(cols - c);   // the rest is the next row's
+        uint32_t m_lo, m;
+        max_split(raw[i], lo, m_lo, m);
+        const uint32_t behind = __shfl_down_sync(0xffffffffu, m_lo, 1, 16), last = __shfl_sync(0xffffffffu, ext_max, i, 16);
+        m = max(m, lane == 15 ? last : behind);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const Shared sh(m);
+        const uint32_t inv = sh.inv_bf16x2();
+        const int b = sh.byte();
+        uint32_t code = split_codes(raw[i], lo, __shfl_up_sync(0xffffffffu, inv, 1, 16), inv);
+        if (__any_sync(0xffffffffu, sh.nan)) {
+            const bool nan_lo = __shfl_up_sync(0xffffffffu, b, 1, 16) == mx4::kNanScale;
+            code &= (nan_lo ? 0u : lo_codes) | (sh.nan ? 0u : ~lo_codes);
+        }
+        const uint32_t next = __shfl_down_sync(0xffffffffu, code, 1, 16);
+        const uint32_t m15 = __shfl_sync(0xffffffffu, m, 15, 16), c15 = __shfl_sync(0xffffffffu, code, 15, 16);
+        if (lane == i) {
+            ext_m = m15;
+            ext_code = c15;
+        }
+        if ((lane & 3) == 0) staged[staged_scale(i * kHalves + half, lane >> 2)] = (uint8_t)b;
+        if (lane < 15 && i * kHalves < out) *reinterpret_cast<uint32_t*>(q) = __funnelshift_r(code, next, 4 * shift);
+        q += (int64_t)kHalves * code_pitch;
+        if (DEQ) {
+            const int b_lo = __shfl_up_sync(0xffffffffu, b, 1, 16);
+            if (i * kHalves < left) {
+                uint32_t w[4 * N];
+                split_values(code, lo, b_lo, b, w);
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    const int at = c - shift + n * V;
-                    if (at >= tile.kt * 128 && at + V <= lim) {
-                        *reinterpret_cast<uint4*>(row + at) = make_uint4(out[4 * n], out[4 * n + 1], out[4 * n + 2], out[4 * n + 3]);
-                    } else if (at < lim) {
+                    const int at = c + n * V;
+                    uint16_t* const to = reinterpret_cast<uint16_t*>(o + n * V);
+                    if (at >= c0 && at + V <= lim) {
+                        *reinterpret_cast<uint4*>(to) = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
+                    } else if (at >= c0) {
+                        if (at < lim) store_before(to, w + 4 * n, (lim - at) * H);
+                    } else if (at + V <= lim) {
+                        store_from(to, w + 4 * n, shift * H);
+                    } else {   // a row within one vector
 #pragma unroll
-                        for (int u = 0; u < V; ++u)
-                            if (at + u >= tile.kt * 128 && at + u < lim) put_element<T, W>(row + at + u, out, n * V + u);
+                        for (int u = 0; u < 8; ++u)
+                            if (u >= shift * H && u < (lim - at) * H) to[u] = (uint16_t)(w[4 * n + u / 2] >> (16 * (u & 1)));
                     }
                 }
-                // the last lane's elements behind its last aligned vector
-                if (lane == 15 && shift != 0) {
-#pragma unroll
-                    for (int u = 8 - V + 1; u < 8; ++u)
-                        if (u >= 8 - shift && c + u < lim) put_element<T, W>(row + c + u, mine, u);
-                }
             }
+            o += step;
+        }
+    }
+    // the rows' last lanes: their codes with the ones behind, and the values of those
+    if (lane < kSegs && lane * kHalves < left) {
+        const Shared sh(ext_m);
+        const uint32_t code = ext.codes(sh);
+        if (c0 + 120 < 2 * code_pitch)
+            *reinterpret_cast<uint32_t*>(codes + (tile.r0 + half + lane * kHalves) * code_pitch + c0 / 2 + 60) =
+                __funnelshift_r(ext_code, code, 4 * shift);
+        if (DEQ && ext_n > 0) {
+            uint32_t w[4 * N];
+            split_values(code, Lo<T>(0), sh.byte(), sh.byte(), w);
+            store_before(reinterpret_cast<uint16_t*>(y + row + lane * step + ext_col), w, ext_n * H);
         }
     }
     store_scale_tile(staged, scales);
@@ -360,8 +469,8 @@ struct Cols<__nv_bfloat16, CPT> {
 #pragma unroll
         for (int t = 0; t < R; ++t) k = absmax_bf16x2(k, v[t].raw);
         if (PAIRED) k = absmax_bf16x2(k, __shfl_xor_sync(0xffffffffu, k, 16));
-        const int lo = scale_byte(k << 16), hi = scale_byte(k & 0xFFFF0000u);
-        const uint32_t s = mx4::inv_scale_bf16x2(lo, hi);
+        const int lo = Shared(k << 16).byte(), hi = Shared(k & 0xFFFF0000u).byte();
+        const uint32_t s = ((uint32_t)(254 - min(lo, 253)) << 7) | ((uint32_t)(254 - min(hi, 253)) << 23);
         b[0] = lo;
         b[CPT - 1] = CPT == 2 ? hi : lo;
 #pragma unroll
@@ -388,14 +497,15 @@ struct Cols<float, 1> {
         float k = 0.f;
 #pragma unroll
         for (int t = 0; t < R; t += 2) k = absmax3(k, v[t].raw, v[t + 1].raw);
-        b[0] = scale_byte(__float_as_uint(k));
-        const float s = inv_scale(b[0]);
+        const Shared sh(__float_as_uint(k));
+        const float s = sh.inv();
+        b[0] = sh.byte();
 #pragma unroll
         for (int w = 0; w < R / 8; ++w) {
             float f[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) f[u] = v[8 * w + u].raw;
-            code[0][w] = b[0] == mx4::kNanScale ? 0u : pack8(f, s);
+            code[0][w] = sh.nan ? 0u : pack8(f, s);
         }
     }
     __device__ static void store(float* p, float a, float) { *p = a; }
@@ -414,8 +524,9 @@ __global__ void __launch_bounds__(512 / CPT, kColCtas<CPT, DEQ>) mx4_cols(const 
     __shared__ __align__(16) uint8_t s_codes[kTile * kStagePitch];
     __shared__ __align__(4) uint8_t s_scale[4 * kTile];   // [column][block]
     constexpr int kLanes = kTile / CPT;      // threads across the columns
-    const int64_t rt = blockIdx.x / (unsigned)col_tiles;   // row tile = k tile of the operand
-    const int ct = (int)(blockIdx.x - rt * col_tiles);
+    const Tile tile(col_tiles);   // the row tile is the operand's k tile
+    const int64_t rt = tile.rt;
+    const int ct = tile.kt;
     const int cl = (threadIdx.x % kLanes) * CPT, blk = threadIdx.x / kLanes;
     const int c = ct * kTile + cl;
     const int64_t r0 = rt * kTile + blk * 32;
@@ -479,21 +590,22 @@ __device__ __forceinline__ void Raw8<float>::put(uint8_t* s, int row, int lane) 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_both(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
+__global__ void __launch_bounds__(kRowThreads<T>, kRowCtas<T>) mx4_both(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
                                                                      uint8_t* __restrict__ codes, int code_pitch,
                                                                      uint8_t* __restrict__ scales, int64_t t_blocks,
                                                                      int64_t t_tiles, uint8_t* __restrict__ t_codes,
                                                                      uint8_t* __restrict__ t_scales) {
+    constexpr int kHalves = kHalvesOf<T>, kSegs = 128 / kHalves;
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* const s_x = smem;
     uint8_t* const s_codes = s_x + kTile * kTile * sizeof(T);
     uint8_t* const s_scale = s_codes + kTile * kStagePitch;
     uint8_t* const staged = s_scale + 4 * kTile;
-    const RowTile tile(tiles_k);
+    const Tile tile(tiles_k);
     {
         const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
         const int c = tile.kt * 128 + lane * 8;
-        const int left = rows_left(tile, rows, half);
+        const int left = rows_left(tile.r0, rows, half);
         const int in = c < cols ? left : 0, out = c / 2 < code_pitch ? left : 0;
         const T* p = x + (tile.r0 + half) * cols + c;
         uint8_t* q = codes + (tile.r0 + half) * code_pitch + c / 2;
@@ -510,9 +622,9 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_both(const T* __
             uint32_t m = raw[i].max_bits();
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const int b = scale_byte(m);
-            const uint32_t code = raw[i].codes(b);
-            if ((lane & 3) == 0) staged[staged_scale(row, lane >> 2)] = (uint8_t)b;
+            const Shared sh(m);
+            const uint32_t code = raw[i].codes(sh);
+            if ((lane & 3) == 0) staged[staged_scale(row, lane >> 2)] = (uint8_t)sh.byte();
             if (i * kHalves < out) *reinterpret_cast<uint32_t*>(q) = code;
             q += (int64_t)kHalves * code_pitch;
         }
@@ -521,24 +633,28 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas<T>) mx4_both(const T* __
     {
         constexpr int CPT = sizeof(T) == 2 ? 2 : 1, R = 32 / CPT, kCols = 32;   // columns and rows a lane, columns a warp
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        const int blk = warp & 3, cl = (warp >> 2) * kCols + (CPT == 2 ? (lane & 15) * 2 : lane);
+        const int blk = warp & 3;
         const int row0 = blk * 32 + (CPT == 2 ? (lane >> 4) * 16 : 0);
-        Cols<T, CPT> v[R];
+#pragma unroll 1
+        for (int h = 0; h < kTile / kCols * 128 / kRowThreads<T>; ++h) {
+            const int cl = ((warp >> 2) + h * (kRowThreads<T> / 128)) * kCols + (CPT == 2 ? (lane & 15) * 2 : lane);
+            Cols<T, CPT> v[R];
 #pragma unroll
-        for (int t = 0; t < R; ++t)
-            v[t].raw = *reinterpret_cast<const decltype(v[t].raw)*>(s_x + chunk_at<T>(row0 + t, cl * (int)sizeof(T) / 16) + cl * sizeof(T) % 16);
-        uint32_t code[CPT][R / 8];
-        int b[CPT];
-        Cols<T, CPT>::template quantize<R, CPT == 2>(v, b, code);
+            for (int t = 0; t < R; ++t)
+                v[t].raw = *reinterpret_cast<const decltype(v[t].raw)*>(s_x + chunk_at<T>(row0 + t, cl * (int)sizeof(T) / 16) + cl * sizeof(T) % 16);
+            uint32_t code[CPT][R / 8];
+            int b[CPT];
+            Cols<T, CPT>::template quantize<R, CPT == 2>(v, b, code);
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            uint8_t* const to = s_codes + (cl + i) * kStagePitch + row0 / 2;
+            for (int i = 0; i < CPT; ++i) {
+                uint8_t* const to = s_codes + (cl + i) * kStagePitch + row0 / 2;
 #pragma unroll
-            for (int w = 0; w < R / 8; w += 2) *reinterpret_cast<uint2*>(to + 4 * w) = make_uint2(code[i][w], code[i][w + 1]);
-            if (CPT == 1 || lane < 16) s_scale[(cl + i) * 4 + blk] = (uint8_t)b[i];
+                for (int w = 0; w < R / 8; w += 2) *reinterpret_cast<uint2*>(to + 4 * w) = make_uint2(code[i][w], code[i][w + 1]);
+                if (CPT == 1 || lane < 16) s_scale[(cl + i) * 4 + blk] = (uint8_t)b[i];
+            }
         }
     }
-    store_col_tile(s_codes, s_scale, tile.r0 / kTile, tile.kt, cols, t_blocks, t_tiles, t_codes, t_scales);
+    store_col_tile(s_codes, s_scale, tile.rt, tile.kt, cols, t_blocks, t_tiles, t_codes, t_scales);
 }
 
 template <typename T, bool DEQ>
@@ -548,8 +664,8 @@ cudaError_t launch_rows(const T* x, int64_t rows, int cols, uint8_t* codes, uint
     const int pitch = (int)(mx4::padded_cols(cols) / 2);
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     prof_begin(st);
-    if (cols % 8 == 0) mx4_rows_vec<T, DEQ><<<(unsigned)grid, kRowThreads, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y);
-    else mx4_rows_any<T, DEQ><<<(unsigned)grid, kRowThreads, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y);
+    if (cols % 8 == 0) mx4_rows_vec<T, DEQ><<<(unsigned)grid, kRowThreads<T>, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y);
+    else mx4_rows_any<T, DEQ><<<(unsigned)grid, kRowThreads<T>, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y);
     prof_end(st, K_MX4_ROWS);
     return cudaGetLastError();
 }
@@ -576,7 +692,7 @@ cudaError_t launch_both(const T* x, int64_t rows, int cols, uint8_t* codes, uint
     const cudaError_t e = cudaFuncSetAttribute(mx4_both<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBothSmem<T>);
     if (e != cudaSuccess) return e;
     prof_begin(st);
-    mx4_both<T><<<(unsigned)grid, kRowThreads, kBothSmem<T>, st>>>(x, rows, cols, tiles_k, codes, (int)(mx4::padded_cols(cols) / 2),
+    mx4_both<T><<<(unsigned)grid, kRowThreads<T>, kBothSmem<T>, st>>>(x, rows, cols, tiles_k, codes, (int)(mx4::padded_cols(cols) / 2),
                                                                    scales, (rows + 31) / 32, mx4::scale_tiles_k(rows), t_codes, t_scales);
     prof_end(st, K_MX4_BOTH);
     return cudaGetLastError();

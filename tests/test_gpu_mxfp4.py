@@ -287,6 +287,34 @@ def test_streams_and_graph_capture(cuda_device):
     jfa.jfa_check_error(ws)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 136, 300])
+def test_quantise_every_place_of_a_row_in_its_vectors(cuda_device, dtype, rows):
+    # narrow rows (several in a vector), rows that end anywhere around a column
+    # tile, with bad blocks beside good ones; a guard behind every buffer
+    rng = np.random.default_rng(rows)
+    for cols in list(range(1, 42)) + list(range(121, 138)) + [255, 257, 1003]:
+        x = draw(rows, cols, dtype, cols)
+        x[torch.from_numpy(rng.random((rows, cols)) < 0.004)] = float("nan")
+        x[torch.from_numpy(rng.random((rows, cols)) < 0.002)] = -float("inf")
+        x[rows // 2] *= 2.0 ** -120
+        nc, ns, n, pad = jfa.jfa_mxfp4_code_bytes(rows, cols), jfa.jfa_mxfp4_scale_bytes(rows, cols), rows * cols, 64
+        for deq in (torch.full((n + pad,), 7.0, dtype=TORCH[dtype], device=cuda_device), None):
+            codes = torch.full((nc + pad,), 0xAA, dtype=torch.uint8, device=cuda_device)
+            scales = torch.full((ns + pad,), 0xEE, dtype=torch.uint8, device=cuda_device)
+            if deq is None:
+                jfa.jfa_quantize_mxfp4(x.to(cuda_device), dtype, rows, cols, 0, codes, scales)
+            else:
+                jfa.jfa_quantize_mxfp4_dequant(x.to(cuda_device), dtype, rows, cols, 0, codes, scales, deq)
+            v = check_operand(jfa.MxOperand(codes[:nc].reshape(rows, -1), scales[:ns], rows, cols), x, False)
+            assert (codes[nc:] == 0xAA).all() and (scales[ns:] == 0xEE).all()
+            if deq is not None:
+                got = deq[:n].reshape(rows, cols).double().cpu().numpy()
+                assert np.array_equal(got, v, equal_nan=True), cols
+                assert np.array_equal(np.signbit(got) & ~np.isnan(v), np.signbit(v) & ~np.isnan(v)), cols
+                assert (deq[n:] == 7.0).all()
+
+
 @pytest.mark.parametrize("along_rows", [False, True])
 def test_quantise_offsets_past_32_bits(cuda_device, along_rows):
     # 2.2e9 elements: the last rows (of whole scale tiles) against the same rows alone
@@ -304,6 +332,18 @@ def test_quantise_offsets_past_32_bits(cuda_device, along_rows):
     else:
         assert torch.equal(op.codes[-128:], alone.codes)
         assert torch.equal(op.scales[-alone.scales.numel():], alone.scales)
+
+
+def test_quantise_offsets_past_32_bits_off_boundaries(cuda_device):
+    rows, cols = 2_240_008, 999
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=cuda_device)
+    x[-136:] = draw(136, cols, "bf16", 1).to(cuda_device)
+    op, deq = jfa.quantize_mxfp4(x, want_dequant=True)
+    alone, d = jfa.quantize_mxfp4(x[-136:].clone(), want_dequant=True)
+    assert rows % 128 == 8 and rows * cols > 1 << 31
+    assert torch.equal(deq[-136:], d) and (deq[:-136] == 0).all()
+    assert torch.equal(op.codes[-136:], alone.codes)
+    assert torch.equal(op.scales[-alone.scales.numel():], alone.scales)
 
 
 def test_product_offsets_past_32_bits(cuda_device):

@@ -335,6 +335,33 @@ jfa_status jfa_matmul_mxfp4(int64_t m, int64_t n, int64_t k, const uint8_t* a_co
                             jfa_dtype out_dtype, int accumulate, void* workspace,
                             size_t ws_bytes, jfa_stream_t stream);
 
+/* A linear layer over MXFP4 operands, each pass in one call (the quantisations
+ * and products above, on one stream).  Forward: y [m][n] = x [m][k] w^T (+ bias)
+ * in the dtype of x; w_codes / w_scales: the weight [n][k] quantised with
+ * along_rows = 0.  Backward: dx [m][k] = dy w in the dtype of dy and dw [n][k]
+ * fp32 = dy^T x (added to what dw holds where accumulate != 0), each product of
+ * operands quantised along its own contraction, the quantiser passed straight
+ * through; wt_codes / wt_scales: the weight with along_rows = 1.  The bias's
+ * gradient is dy summed over its rows.
+ * scratch: jfa_linear_mxfp4_scratch_bytes(m, n, k, backward) bytes, 16-byte
+ * aligned, any contents, for the operands that the call quantises (0 for a
+ * size outside [0, 2^30]); calls that run side by side need one each.
+ * workspace as of jfa_matmul_mxfp4.  All tensors 16-byte aligned, bias 4-byte
+ * aligned or NULL.  m, n, k in [0, 2^30]; without tokens dw is zero, or
+ * unchanged where it accumulates. */
+size_t jfa_linear_mxfp4_scratch_bytes(int64_t m, int64_t n, int64_t k, int backward);
+jfa_status jfa_linear_mxfp4_forward(const void* x, jfa_dtype dtype, int64_t m, int64_t n,
+                                    int64_t k, const uint8_t* w_codes, const uint8_t* w_scales,
+                                    const float* bias, void* y, void* scratch,
+                                    size_t scratch_bytes, void* workspace, size_t ws_bytes,
+                                    jfa_stream_t stream);
+jfa_status jfa_linear_mxfp4_backward(const void* dy, jfa_dtype dtype, const void* x,
+                                     jfa_dtype x_dtype, int64_t m, int64_t n, int64_t k,
+                                     const uint8_t* wt_codes, const uint8_t* wt_scales, void* dx,
+                                     float* dw, int accumulate, void* scratch,
+                                     size_t scratch_bytes, void* workspace, size_t ws_bytes,
+                                     jfa_stream_t stream);
+
 /* The norms before and after a block (an attention or MLP block of the model
  * the attention runs in), fused with the block's gate and residual scale.
  * For each row of `dim` elements of the residual stream x, the block's output

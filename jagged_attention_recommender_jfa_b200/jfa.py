@@ -15,7 +15,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import itertools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -47,7 +46,8 @@ EXPORTS = ("jfa_workspace_bytes", "jfa_forward", "jfa_backward", "jfa_quantize_m
            "jfa_norm_quantize_mxfp8", "jfa_mxfp4_code_bytes", "jfa_mxfp4_scale_bytes",
            "jfa_mxfp4_workspace_bytes", "jfa_quantize_mxfp4", "jfa_quantize_mxfp4_dequant",
            "jfa_quantize_mxfp4_both",
-           "jfa_matmul_mxfp4", "jfa_block_norm_workspace_bytes", "jfa_block_norm_forward",
+           "jfa_matmul_mxfp4", "jfa_linear_mxfp4_scratch_bytes", "jfa_linear_mxfp4_forward",
+           "jfa_linear_mxfp4_backward", "jfa_block_norm_workspace_bytes", "jfa_block_norm_forward",
            "jfa_block_norm_backward")
 NORM = {"none": 0, "rms": 1, "layer": 2}
 GATE = {"none": 0, "identity": 1, "silu": 2, "sigmoid": 3}
@@ -147,6 +147,13 @@ def load():
         lib.jfa_quantize_mxfp4_both.restype = i32
         lib.jfa_matmul_mxfp4.argtypes = [i64, i64, i64, P, P, P, P, P, P, i32, i32, P, sz, P]
         lib.jfa_matmul_mxfp4.restype = i32
+        lib.jfa_linear_mxfp4_scratch_bytes.argtypes = [i64, i64, i64, i32]
+        lib.jfa_linear_mxfp4_scratch_bytes.restype = sz
+        lib.jfa_linear_mxfp4_forward.argtypes = [P, i32, i64, i64, i64, P, P, P, P, P, sz, P, sz, P]
+        lib.jfa_linear_mxfp4_forward.restype = i32
+        lib.jfa_linear_mxfp4_backward.argtypes = [P, i32, P, i32, i64, i64, i64, P, P, P, P, i32, P, sz,
+                                                  P, sz, P]
+        lib.jfa_linear_mxfp4_backward.restype = i32
         PN = ctypes.POINTER(jfa_block_norm)
         lib.jfa_block_norm_workspace_bytes.argtypes = [PN]
         lib.jfa_block_norm_workspace_bytes.restype = sz
@@ -373,6 +380,33 @@ def jfa_matmul_mxfp4(m, n, k, a_codes, a_scales, b_codes, b_scales, bias, out, o
                                    _addr(b_codes), _addr(b_scales), _addr(bias), _addr(out),
                                    DTYPE.get(out_dtype, out_dtype), int(bool(accumulate)),
                                    _addr(workspace), int(ws_bytes), _stream(stream)))
+
+
+def _nbytes(t, given=None) -> int:
+    return int(given) if given is not None else t.numel() * t.element_size()
+
+
+def jfa_linear_mxfp4_scratch_bytes(m, n, k, backward) -> int:
+    return int(load().jfa_linear_mxfp4_scratch_bytes(int(m), int(n), int(k), int(bool(backward))))
+
+
+def jfa_linear_mxfp4_forward(x, dtype, m, n, k, w_codes, w_scales, bias, y, scratch, workspace,
+                             scratch_bytes=None, ws_bytes=None, stream=None):
+    _check(load().jfa_linear_mxfp4_forward(_addr(x), DTYPE.get(dtype, dtype), int(m), int(n), int(k),
+                                           _addr(w_codes), _addr(w_scales), _addr(bias), _addr(y),
+                                           _addr(scratch), _nbytes(scratch, scratch_bytes),
+                                           _addr(workspace), _nbytes(workspace, ws_bytes),
+                                           _stream(stream)))
+
+
+def jfa_linear_mxfp4_backward(dy, dtype, x, x_dtype, m, n, k, wt_codes, wt_scales, dx, dw, accumulate,
+                              scratch, workspace, scratch_bytes=None, ws_bytes=None, stream=None):
+    _check(load().jfa_linear_mxfp4_backward(_addr(dy), DTYPE.get(dtype, dtype), _addr(x),
+                                            DTYPE.get(x_dtype, x_dtype), int(m), int(n), int(k),
+                                            _addr(wt_codes), _addr(wt_scales), _addr(dx), _addr(dw),
+                                            int(bool(accumulate)), _addr(scratch),
+                                            _nbytes(scratch, scratch_bytes), _addr(workspace),
+                                            _nbytes(workspace, ws_bytes), _stream(stream)))
 
 
 def make_block_norm(*, rows, dim, dtype="bf16", post_norm="rms", pre_norm="rms", gate="silu",
@@ -653,15 +687,6 @@ def _ws_on(ws, index):
     return ws
 
 
-def _product(m, n, k, a, a_scales, b, b_scales, bias, out, accumulate, ws, s):
-    """jfa_matmul_mxfp4 on checked arguments; the operands are addresses."""
-    st = (_LIB or load()).jfa_matmul_mxfp4(
-        m, n, k, a, a_scales, b, b_scales, _ptr(bias), out.data_ptr(), _TORCH_DTYPE[out.dtype],
-        1 if accumulate else 0, ws.data_ptr(), ws.numel() * ws.element_size(), s)
-    if st:
-        _check(st)
-
-
 def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torch.bfloat16,
                  accumulate=False, ws=None, stream=None, check=True):
     """``a`` [m, k] times the transpose of ``b`` [n, k] (+ ``bias`` [n] fp32),
@@ -688,8 +713,12 @@ def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torc
     ws = _ws_on(ws, index)
     if out is None:
         out = torch.empty(m, n, dtype=out_dtype, device=a_codes.device)
-    _product(m, n, k, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
-             bias, out, accumulate, ws, s)
+    st = (_LIB or load()).jfa_matmul_mxfp4(
+        m, n, k, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
+        _ptr(bias), out.data_ptr(), _TORCH_DTYPE[out.dtype], 1 if accumulate else 0, ws.data_ptr(),
+        ws.numel() * ws.element_size(), s)
+    if st:
+        _check(st)
     if check:
         jfa_check_error(ws, s)
     return out
@@ -709,19 +738,17 @@ def linear_mxfp4_forward(x, w: MxOperand, bias=None, ws=None, stream=None, check
         with _switch(x.device, stream):
             return linear_mxfp4_forward(x, w, bias, ws, None, check)
     ws = _ws_on(ws, index)
-    code_bytes = m * _code_pitch(k)
-    buf = torch.empty(code_bytes + _scale_bytes(m, k), dtype=_U8, device=x.device)   # codes, then scales
-    codes = buf.data_ptr()
-    st = (_LIB or load()).jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 0, codes,
-                                             codes + code_bytes, s)
+    # room for x's codes, then its scales
+    buf = torch.empty(m * _code_pitch(k) + _scale_bytes(m, k), dtype=_U8, device=x.device)
+    y = torch.empty(m, n, dtype=x.dtype, device=x.device)
+    st = (_LIB or load()).jfa_linear_mxfp4_forward(
+        x.data_ptr(), _TORCH_DTYPE[x.dtype], m, n, k, w_codes.data_ptr(), w_scales.data_ptr(), _ptr(bias),
+        y.data_ptr(), buf.data_ptr(), buf.numel(), ws.data_ptr(), ws.numel() * ws.element_size(), s)
     if st:
         _check(st)
-    out = torch.empty(m, n, dtype=x.dtype, device=x.device)
-    _product(m, n, k, codes, codes + code_bytes, w_codes.data_ptr(), w_scales.data_ptr(), bias, out,
-             False, ws, s)
     if check:
         jfa_check_error(ws, s)
-    return out
+    return y
 
 
 def linear_mxfp4_backward(dy, x, w_t: MxOperand, dw=None, ws=None, stream=None, check=True):
@@ -746,19 +773,19 @@ def linear_mxfp4_backward(dy, x, w_t: MxOperand, dw=None, ws=None, stream=None, 
         with _switch(dy.device, stream):
             return linear_mxfp4_backward(dy, x, w_t, dw, ws, None, check)
     ws = _ws_on(ws, index)
-    lib, dev = load(), dy.device
-    # one buffer: the codes and scales of dy, of its transpose and of x's
-    sizes = [m * _code_pitch(n), _scale_bytes(m, n), n * _code_pitch(m), _scale_bytes(n, m), k * _code_pitch(m),
-             _scale_bytes(k, m)]
-    buf = torch.empty(sum(sizes), dtype=_U8, device=dev)
-    a, a_s, t, t_s, b, b_s = itertools.accumulate([buf.data_ptr()] + sizes[:-1])
-    _check(lib.jfa_quantize_mxfp4_both(dy.data_ptr(), _TORCH_DTYPE[dy.dtype], m, n, a, a_s, t, t_s, s))
+    dev = dy.device
+    # room for the operands of dy, of its transpose and of x's
+    buf = torch.empty(m * _code_pitch(n) + _scale_bytes(m, n) + (n + k) * _code_pitch(m) + _scale_bytes(n, m)
+                      + _scale_bytes(k, m), dtype=_U8, device=dev)
     dx = torch.empty(m, k, dtype=dy.dtype, device=dev)
-    _product(m, k, n, a, a_s, w_codes.data_ptr(), w_scales.data_ptr(), None, dx, False, ws, s)
-    _check(lib.jfa_quantize_mxfp4(x.data_ptr(), _TORCH_DTYPE[x.dtype], m, k, 1, b, b_s, s))
     if not accumulate:
         dw = torch.empty(n, k, dtype=torch.float32, device=dev)
-    _product(n, k, m, t, t_s, b, b_s, None, dw, accumulate, ws, s)
+    st = (_LIB or load()).jfa_linear_mxfp4_backward(
+        dy.data_ptr(), _TORCH_DTYPE[dy.dtype], x.data_ptr(), _TORCH_DTYPE[x.dtype], m, n, k,
+        w_codes.data_ptr(), w_scales.data_ptr(), dx.data_ptr(), dw.data_ptr(), 1 if accumulate else 0,
+        buf.data_ptr(), buf.numel(), ws.data_ptr(), ws.numel() * ws.element_size(), s)
+    if st:
+        _check(st)
     if check:
         jfa_check_error(ws, s)
     return dx, dw

@@ -254,6 +254,39 @@ def test_linear_forward_and_backward(cuda_device, m, n, k, dtype):
         assert (np.abs(got.double().cpu().numpy() - r) <= bound).all(), name
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 64, 64), (37, 66, 131), (300, 257, 100), (5, 0, 40), (5, 40, 0), (0, 40, 33)])
+@pytest.mark.parametrize("accumulate", [0, 1])
+def test_linear_entries_equal_their_parts(cuda_device, m, n, k, accumulate):
+    # the one-call passes write what the quantiser and the product write, and
+    # nothing behind their buffers
+    dev, pad = cuda_device, 64
+    x, w, dy = (draw(*s, "bf16", i).to(dev) for i, s in enumerate([(m, k), (n, k), (m, n)]))
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(1)).to(dev)
+    wq, wt, ws = jfa.quantize_mxfp4(w), jfa.quantize_mxfp4(w, along_rows=True), jfa.mxfp4_workspace(dev)
+
+    def guarded(count, dtype, value):
+        return torch.full((count + pad,), value, dtype=dtype, device=dev)
+
+    def left_alone(*pairs):
+        return all((t[count:] == value).all() for t, count, value in pairs)
+
+    ny, nx, nw = m * n, m * k, n * k
+    sizes = [jfa.jfa_linear_mxfp4_scratch_bytes(m, n, k, b) for b in (0, 1)]
+    s0, s1 = (guarded(c, torch.uint8, 0xEE) for c in sizes)
+    y, dx = guarded(ny, torch.bfloat16, 7.0), guarded(nx, torch.bfloat16, 7.0)
+    dw = guarded(nw, torch.float32, 0.5)
+    jfa.jfa_linear_mxfp4_forward(x, "bf16", m, n, k, wq.codes, wq.scales, bias, y, s0, ws, scratch_bytes=sizes[0])
+    jfa.jfa_linear_mxfp4_backward(dy, "bf16", x, "bf16", m, n, k, wt.codes, wt.scales, dx, dw, accumulate, s1, ws,
+                                  scratch_bytes=sizes[1])
+    jfa.jfa_check_error(ws)
+    assert left_alone((s0, sizes[0], 0xEE), (s1, sizes[1], 0xEE), (y, ny, 7.0), (dx, nx, 7.0), (dw, nw, 0.5))
+    g, gt, xt = jfa.quantize_mxfp4(dy), jfa.quantize_mxfp4(dy, True), jfa.quantize_mxfp4(x, True)
+    held = torch.full((n, k), 0.5, device=dev)
+    assert torch.equal(y[:ny].view(m, n), jfa.matmul_mxfp4(jfa.quantize_mxfp4(x), wq, bias))
+    assert torch.equal(dx[:nx].view(m, k), jfa.matmul_mxfp4(g, wt))
+    assert torch.equal(dw[:nw].view(n, k), jfa.matmul_mxfp4(gt, xt, out=held, accumulate=bool(accumulate)))
+
+
 def test_linear_of_no_tokens(cuda_device):
     x, dy = (torch.zeros(0, c, dtype=torch.bfloat16, device=cuda_device) for c in (64, 96))
     w = draw(96, 64, "bf16", 1).to(cuda_device)

@@ -75,6 +75,41 @@ def test_product_refusals(change, status):
     refused(status, jfa.jfa_matmul_mxfp4, **a, stream=0)
 
 
+@pytest.mark.parametrize("change,status", [
+    (dict(m=-1), INVALID), (dict(n=(1 << 30) + 1), INVALID), (dict(k=-1), INVALID), (dict(dtype=2), INVALID),
+    (dict(x=None), INVALID), (dict(x=FAKE + 8), INVALID), (dict(w_codes=None), INVALID), (dict(w_scales=None), INVALID),
+    (dict(w_codes=FAKE + 4), INVALID), (dict(y=None), INVALID), (dict(y=FAKE + 2), INVALID), (dict(bias=FAKE + 2), INVALID),
+    (dict(scratch=None), INVALID), (dict(scratch=FAKE + 8), INVALID), (dict(scratch_bytes=575), WORKSPACE),
+    (dict(workspace=None), INVALID), (dict(workspace=FAKE + 8), INVALID), (dict(ws_bytes=255), WORKSPACE)])
+def test_linear_forward_refusals(change, status):
+    assert jfa.jfa_linear_mxfp4_scratch_bytes(4, 8, 32, 0) == 4 * 16 + 512
+    a = dict(x=FAKE, dtype="bf16", m=4, n=8, k=32, w_codes=FAKE, w_scales=FAKE, bias=None, y=FAKE, scratch=FAKE,
+             scratch_bytes=576, workspace=FAKE, ws_bytes=256)
+    refused(status, jfa.jfa_linear_mxfp4_forward, **{**a, **change}, stream=0)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(m=(1 << 30) + 1), INVALID), (dict(n=-1), INVALID), (dict(k=-1), INVALID), (dict(dtype=2), INVALID),
+    (dict(x_dtype=3), INVALID), (dict(dy=None), INVALID), (dict(x=None), INVALID), (dict(x=FAKE + 8), INVALID),
+    (dict(wt_codes=None), INVALID), (dict(wt_scales=FAKE + 1), INVALID), (dict(dx=None), INVALID),
+    (dict(dw=None), INVALID), (dict(dw=FAKE + 4), INVALID), (dict(scratch=None), INVALID),
+    (dict(scratch_bytes=2239), WORKSPACE), (dict(workspace=None), INVALID), (dict(ws_bytes=0), WORKSPACE)])
+def test_linear_backward_refusals(change, status):
+    # dy 4 x 8, its transpose and x's (32 x 4)
+    assert jfa.jfa_linear_mxfp4_scratch_bytes(4, 8, 32, 1) == (4 + 8 + 32) * 16 + 3 * 512 == 2240
+    a = dict(dy=FAKE, dtype="bf16", x=FAKE, x_dtype="f32", m=4, n=8, k=32, wt_codes=FAKE, wt_scales=FAKE, dx=FAKE, dw=FAKE,
+             accumulate=0, scratch=FAKE, scratch_bytes=2240, workspace=FAKE, ws_bytes=256)
+    refused(status, jfa.jfa_linear_mxfp4_backward, **{**a, **change}, stream=0)
+
+
+def test_linear_of_nothing_is_a_no_op():
+    assert jfa.jfa_linear_mxfp4_scratch_bytes(-1, 8, 8, 0) == jfa.jfa_linear_mxfp4_scratch_bytes(8, 8, (1 << 30) + 1, 1) == 0
+    jfa.jfa_linear_mxfp4_forward(None, "bf16", 0, 8, 32, None, None, None, None, None, FAKE, 0, 256, stream=0)
+    jfa.jfa_linear_mxfp4_forward(FAKE, "bf16", 3, 0, 32, None, None, None, None, FAKE, FAKE, 1 << 20, 256, stream=0)
+    jfa.jfa_linear_mxfp4_backward(FAKE, "f32", None, "f32", 3, 8, 0, None, None, None, None, 0, FAKE, FAKE, 1 << 20, 256,
+                                  stream=0)
+
+
 def test_product_of_nothing_is_a_no_op():
     assert jfa.jfa_mxfp4_workspace_bytes() == 256
     for m, n in ((0, 8), (8, 0)):

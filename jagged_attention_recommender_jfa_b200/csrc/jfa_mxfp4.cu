@@ -56,7 +56,9 @@ struct Raw8<__nv_bfloat16> {
         scaled(r.w, s, f[6], f[7]);
         return sh.nan ? 0u : cvt8(f);
     }
-    // to the shared tile of mx4_both
+    // to shared memory: the eight, the first vector of them, and into the tile of mx4_both
+    __device__ __forceinline__ void put_vectors(uint8_t* s) const { *reinterpret_cast<uint4*>(s) = r; }
+    __device__ __forceinline__ void put_vector(uint8_t* s) const { *reinterpret_cast<uint4*>(s) = r; }
     __device__ __forceinline__ void put(uint8_t* s, int row, int lane) const;
 };
 template <>
@@ -81,6 +83,11 @@ struct Raw8<float> {
         const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         return sh.nan ? 0u : pack8(f, sh.inv());
     }
+    __device__ __forceinline__ void put_vectors(uint8_t* s) const {
+        reinterpret_cast<float4*>(s)[0] = a;
+        reinterpret_cast<float4*>(s)[1] = b;
+    }
+    __device__ __forceinline__ void put_vector(uint8_t* s) const { *reinterpret_cast<float4*>(s) = a; }
     __device__ __forceinline__ void put(uint8_t* s, int row, int lane) const;
 };
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
@@ -283,148 +290,6 @@ __device__ __forceinline__ void store_before(uint16_t* p, const uint32_t* w, int
     if (s & 1) p[s - 1] = (uint16_t)(s & 4 ? (s & 2 ? w[3] : w[2]) : (s & 2 ? w[1] : w[0]));
 }
 
-template <typename T, bool DEQ>
-__global__ void __launch_bounds__(kRowThreads<T>, kAnyCtas<T>) mx4_rows_any(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
-                                                                         uint8_t* __restrict__ codes, int code_pitch,
-                                                                         uint8_t* __restrict__ scales, T* __restrict__ y) {
-    constexpr int kHalves = kHalvesOf<T>, kSegs = 128 / kHalves;
-    constexpr int V = 16 / sizeof(T), N = 8 / V, H = sizeof(T) / 2;   // elements of a vector, vectors of eight, half words
-    __shared__ __align__(16) uint8_t staged[512];
-    const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
-    const Tile tile(tiles_k);
-    const int left = rows_left(tile.r0, rows, half);
-    const int c0 = tile.kt * 128, lim = min(cols, c0 + 128);
-    const int64_t row = (tile.r0 + half) * cols, step = (int64_t)kHalves * cols;
-    const int shift = (int)(row & (V - 1)), c = c0 + lane * 8 - shift;   // the lane's first column
-    const T* const end = x + rows * cols;
-    const T* p = x + row + c;
-    // eight elements' worth of vectors, or one vector
-    auto load = [&](Raw8<T>& e, const T* from, int col, bool one) {
-        uint32_t w[4 * N];
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if ((n == 0 || !one) && col + n * V < cols) {
-                if (from + (n + 1) * V <= end) {
-                    v = __ldg(reinterpret_cast<const uint4*>(from + n * V));
-                } else {
-                    T* t = reinterpret_cast<T*>(&v);   // the tensor ends inside this vector
-#pragma unroll
-                    for (int u = 0; u < V; ++u)
-                        if (from + n * V + u < end) t[u] = from[n * V + u];
-                }
-            }
-            w[4 * n] = v.x;
-            w[4 * n + 1] = v.y;
-            w[4 * n + 2] = v.z;
-            w[4 * n + 3] = v.w;
-        }
-        e.words(w);
-    };
-    Raw8<T> raw[kSegs], ext;
-    if (tile.r0 + 128 + 8 <= rows) {   // eight rows more are at least a vector
-#pragma unroll
-        for (int i = 0; i < kSegs; ++i) {
-            uint32_t w[4 * N] = {};
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-                if (c + n * V < cols) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + n * V));
-                    w[4 * n] = v.x;
-                    w[4 * n + 1] = v.y;
-                    w[4 * n + 2] = v.z;
-                    w[4 * n + 3] = v.w;
-                }
-            raw[i].words(w);
-            p += step;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kSegs; ++i) {
-            if (i * kHalves < left) load(raw[i], p, c, false);
-            p += step;
-        }
-    }
-    // lane i < kSegs: the vector behind row i's last lane
-    const int ext_col = c0 + 128 - shift, ext_n = min(max(cols - ext_col, 0), shift);
-    if (lane < kSegs && lane * kHalves < left && ext_n > 0) load(ext, x + row + lane * step + ext_col, ext_col, true);
-    ext.clip(ext_n);
-    const uint32_t ext_max = ext.max_bits();
-
-    const int lo_n = lane & 3 ? 0 : shift;
-    const Lo<T> lo(lo_n);
-    const uint32_t lo_codes = (1u << (4 * lo_n)) - 1u;
-    uint8_t* q = codes + (tile.r0 + half) * code_pitch + c0 / 2 + lane * 4;
-    const int out = c0 + lane * 8 < 2 * code_pitch ? left : 0;
-    T* o = y + row + c;
-    uint32_t ext_m = 0u, ext_code = 0u;
-#pragma unroll
-    for (int i = 0; i < kSegs; ++i) {
-        if (c + 8 > cols) raw[i].clip(cols - c);   // the rest is the next row's
-        uint32_t m_lo, m;
-        max_split(raw[i], lo, m_lo, m);
-        const uint32_t behind = __shfl_down_sync(0xffffffffu, m_lo, 1, 16), last = __shfl_sync(0xffffffffu, ext_max, i, 16);
-        m = max(m, lane == 15 ? last : behind);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const Shared sh(m);
-        const uint32_t inv = sh.inv_bf16x2();
-        const int b = sh.byte();
-        uint32_t code = split_codes(raw[i], lo, __shfl_up_sync(0xffffffffu, inv, 1, 16), inv);
-        if (__any_sync(0xffffffffu, sh.nan)) {
-            const bool nan_lo = __shfl_up_sync(0xffffffffu, b, 1, 16) == mx4::kNanScale;
-            code &= (nan_lo ? 0u : lo_codes) | (sh.nan ? 0u : ~lo_codes);
-        }
-        const uint32_t next = __shfl_down_sync(0xffffffffu, code, 1, 16);
-        const uint32_t m15 = __shfl_sync(0xffffffffu, m, 15, 16), c15 = __shfl_sync(0xffffffffu, code, 15, 16);
-        if (lane == i) {
-            ext_m = m15;
-            ext_code = c15;
-        }
-        if ((lane & 3) == 0) staged[staged_scale(i * kHalves + half, lane >> 2)] = (uint8_t)b;
-        if (lane < 15 && i * kHalves < out) *reinterpret_cast<uint32_t*>(q) = __funnelshift_r(code, next, 4 * shift);
-        q += (int64_t)kHalves * code_pitch;
-        if (DEQ) {
-            const int b_lo = __shfl_up_sync(0xffffffffu, b, 1, 16);
-            if (i * kHalves < left) {
-                uint32_t w[4 * N];
-                split_values(code, lo, b_lo, b, w);
-#pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const int at = c + n * V;
-                    uint16_t* const to = reinterpret_cast<uint16_t*>(o + n * V);
-                    if (at >= c0 && at + V <= lim) {
-                        *reinterpret_cast<uint4*>(to) = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
-                    } else if (at >= c0) {
-                        if (at < lim) store_before(to, w + 4 * n, (lim - at) * H);
-                    } else if (at + V <= lim) {
-                        store_from(to, w + 4 * n, shift * H);
-                    } else {   // a row within one vector
-#pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            if (u >= shift * H && u < (lim - at) * H) to[u] = (uint16_t)(w[4 * n + u / 2] >> (16 * (u & 1)));
-                    }
-                }
-            }
-            o += step;
-        }
-    }
-    // the rows' last lanes: their codes with the ones behind, and the values of those
-    if (lane < kSegs && lane * kHalves < left) {
-        const Shared sh(ext_m);
-        const uint32_t code = ext.codes(sh);
-        if (c0 + 120 < 2 * code_pitch)
-            *reinterpret_cast<uint32_t*>(codes + (tile.r0 + half + lane * kHalves) * code_pitch + c0 / 2 + 60) =
-                __funnelshift_r(ext_code, code, 4 * shift);
-        if (DEQ && ext_n > 0) {
-            uint32_t w[4 * N];
-            split_values(code, Lo<T>(0), sh.byte(), sh.byte(), w);
-            store_before(reinterpret_cast<uint16_t*>(y + row + lane * step + ext_col), w, ext_n * H);
-        }
-    }
-    store_scale_tile(staged, scales);
-}
-
 // The operand of the transpose: blocks are 32 consecutive rows of a column.
 // A CTA takes 128 rows x 128 columns, which is one 512-byte scale tile of the
 // result; a thread holds 32 rows of CPT adjacent columns (all 32 loads in
@@ -463,6 +328,9 @@ struct Cols<__nv_bfloat16, CPT> {
     __device__ void load(const __nv_bfloat16* p) {
         raw = CPT == 2 ? __ldg(reinterpret_cast<const unsigned int*>(p)) : __ldg(reinterpret_cast<const unsigned short*>(p));
     }
+    __device__ void take(const uint8_t* s) {   // from shared memory
+        raw = CPT == 2 ? *reinterpret_cast<const uint32_t*>(s) : *reinterpret_cast<const uint16_t*>(s);
+    }
     template <int R, bool PAIRED>
     __device__ static void quantize(const Cols (&v)[R], int (&b)[CPT], uint32_t (&code)[CPT][R / 8]) {
         uint32_t k = 0;
@@ -491,6 +359,7 @@ template <>
 struct Cols<float, 1> {
     float raw = 0.f;
     __device__ void load(const float* p) { raw = __ldg(p); }
+    __device__ void take(const uint8_t* s) { raw = *reinterpret_cast<const float*>(s); }
     template <int R, bool PAIRED>
     __device__ static void quantize(const Cols (&v)[R], int (&b)[1], uint32_t (&code)[1][R / 8]) {
         static_assert(!PAIRED, "a lane holds whole blocks");
@@ -567,6 +436,184 @@ __global__ void __launch_bounds__(512 / CPT, kColCtas<CPT, DEQ>) mx4_cols(const 
     store_col_tile(s_codes, s_scale, rt, ct, cols, blocks_k, tiles_k, codes, scales);
 }
 
+// BOTH: the operand of the transpose as well; the elements go through shared
+// memory as the vectors hold them, a row of the tile 16 bytes longer than its
+// 128 elements, and a lane then takes 32 rows of a column.  One pass instead of
+// two: 65537 x 1003 bf16 97 -> 68 us, fp32 122 -> 91, 65537 x 4093 bf16 337 ->
+// 240.
+template <typename T>
+constexpr int kAnyPitch = kTile * (int)sizeof(T) + 16;
+template <typename T>
+constexpr int kBothAnySmem = kTile * (kAnyPitch<T> + kStagePitch + 4);
+
+template <typename T, bool DEQ, bool BOTH>
+__global__ void __launch_bounds__(kRowThreads<T>, kAnyCtas<T>) mx4_rows_any(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
+                                                                         uint8_t* __restrict__ codes, int code_pitch,
+                                                                         uint8_t* __restrict__ scales, T* __restrict__ y,
+                                                                         int64_t t_blocks, int64_t t_tiles,
+                                                                         uint8_t* __restrict__ t_codes,
+                                                                         uint8_t* __restrict__ t_scales) {
+    extern __shared__ __align__(16) uint8_t smem[];   // BOTH: elements, codes and scales of the columns
+    constexpr int kHalves = kHalvesOf<T>, kSegs = 128 / kHalves;
+    constexpr int V = 16 / sizeof(T), N = 8 / V, H = sizeof(T) / 2;   // elements of a vector, vectors of eight, half words
+    __shared__ __align__(16) uint8_t staged[512];
+    const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
+    const Tile tile(tiles_k);
+    const int left = rows_left(tile.r0, rows, half);
+    const int c0 = tile.kt * 128, lim = min(cols, c0 + 128);
+    const int64_t row = (tile.r0 + half) * cols, step = (int64_t)kHalves * cols;
+    const int shift = (int)(row & (V - 1)), c = c0 + lane * 8 - shift;   // the lane's first column
+    const T* const end = x + rows * cols;
+    const T* p = x + row + c;
+    // eight elements' worth of vectors, or one vector
+    auto load = [&](Raw8<T>& e, const T* from, int col, bool one) {
+        uint32_t w[4 * N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if ((n == 0 || !one) && col + n * V < cols) {
+                if (from + (n + 1) * V <= end) {
+                    v = __ldg(reinterpret_cast<const uint4*>(from + n * V));
+                } else {
+                    T* t = reinterpret_cast<T*>(&v);   // the tensor ends inside this vector
+#pragma unroll
+                    for (int u = 0; u < V; ++u)
+                        if (from + n * V + u < end) t[u] = from[n * V + u];
+                }
+            }
+            w[4 * n] = v.x;
+            w[4 * n + 1] = v.y;
+            w[4 * n + 2] = v.z;
+            w[4 * n + 3] = v.w;
+        }
+        e.words(w);
+    };
+    Raw8<T> raw[kSegs], ext;
+    if (tile.r0 + 128 + 8 <= rows) {   // eight rows more are at least a vector
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+            uint32_t w[4 * N] = {};
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                if (c + n * V < cols) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + n * V));
+                    w[4 * n] = v.x;
+                    w[4 * n + 1] = v.y;
+                    w[4 * n + 2] = v.z;
+                    w[4 * n + 3] = v.w;
+                }
+            raw[i].words(w);
+            p += step;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+            if (i * kHalves < left) load(raw[i], p, c, false);
+            p += step;
+        }
+    }
+    // lane i < kSegs: the vector behind row i's last lane
+    const int ext_col = c0 + 128 - shift, ext_n = min(max(cols - ext_col, 0), shift);
+    if (lane < kSegs && lane * kHalves < left && ext_n > 0) load(ext, x + row + lane * step + ext_col, ext_col, true);
+    ext.clip(ext_n);
+    const uint32_t ext_max = ext.max_bits();
+
+    const int lo_n = lane & 3 ? 0 : shift;
+    const Lo<T> lo(lo_n);
+    const uint32_t lo_codes = (1u << (4 * lo_n)) - 1u;
+    uint8_t* q = codes + (tile.r0 + half) * code_pitch + c0 / 2 + lane * 4;
+    const int out = c0 + lane * 8 < 2 * code_pitch ? left : 0;
+    T* o = y + row + c;
+    uint32_t ext_m = 0u, ext_code = 0u;
+#pragma unroll
+    for (int i = 0; i < kSegs; ++i) {
+        if (c + 8 > cols) raw[i].clip(cols - c);   // the rest is the next row's
+        if (BOTH) raw[i].put_vectors(smem + (i * kHalves + half) * kAnyPitch<T> + lane * 8 * (int)sizeof(T));
+        uint32_t m_lo, m;
+        max_split(raw[i], lo, m_lo, m);
+        const uint32_t behind = __shfl_down_sync(0xffffffffu, m_lo, 1, 16), last = __shfl_sync(0xffffffffu, ext_max, i, 16);
+        m = max(m, lane == 15 ? last : behind);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const Shared sh(m);
+        const uint32_t inv = sh.inv_bf16x2();
+        const int b = sh.byte();
+        uint32_t code = split_codes(raw[i], lo, __shfl_up_sync(0xffffffffu, inv, 1, 16), inv);
+        if (__any_sync(0xffffffffu, sh.nan)) {
+            const bool nan_lo = __shfl_up_sync(0xffffffffu, b, 1, 16) == mx4::kNanScale;
+            code &= (nan_lo ? 0u : lo_codes) | (sh.nan ? 0u : ~lo_codes);
+        }
+        const uint32_t next = __shfl_down_sync(0xffffffffu, code, 1, 16);
+        const uint32_t m15 = __shfl_sync(0xffffffffu, m, 15, 16), c15 = __shfl_sync(0xffffffffu, code, 15, 16);
+        if (lane == i) {
+            ext_m = m15;
+            ext_code = c15;
+        }
+        if ((lane & 3) == 0) staged[staged_scale(i * kHalves + half, lane >> 2)] = (uint8_t)b;
+        if (lane < 15 && i * kHalves < out) *reinterpret_cast<uint32_t*>(q) = __funnelshift_r(code, next, 4 * shift);
+        q += (int64_t)kHalves * code_pitch;
+        if (DEQ) {
+            const int b_lo = __shfl_up_sync(0xffffffffu, b, 1, 16);
+            if (i * kHalves < left) {
+                uint32_t w[4 * N];
+                split_values(code, lo, b_lo, b, w);
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const int at = c + n * V;
+                    uint16_t* const to = reinterpret_cast<uint16_t*>(o + n * V);
+                    if (at >= c0 && at + V <= lim) {
+                        *reinterpret_cast<uint4*>(to) = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
+                    } else if (at >= c0) {
+                        if (at < lim) store_before(to, w + 4 * n, (lim - at) * H);
+                    } else if (at + V <= lim) {
+                        store_from(to, w + 4 * n, shift * H);
+                    } else {   // a row within one vector
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            if (u >= shift * H && u < (lim - at) * H) to[u] = (uint16_t)(w[4 * n + u / 2] >> (16 * (u & 1)));
+                    }
+                }
+            }
+            o += step;
+        }
+    }
+    if (BOTH && lane < kSegs) ext.put_vector(smem + (lane * kHalves + half) * kAnyPitch<T> + kTile * (int)sizeof(T));
+    // the rows' last lanes: their codes with the ones behind, and the values of those
+    if (lane < kSegs && lane * kHalves < left) {
+        const Shared sh(ext_m);
+        const uint32_t code = ext.codes(sh);
+        if (c0 + 120 < 2 * code_pitch)
+            *reinterpret_cast<uint32_t*>(codes + (tile.r0 + half + lane * kHalves) * code_pitch + c0 / 2 + 60) =
+                __funnelshift_r(ext_code, code, 4 * shift);
+        if (DEQ && ext_n > 0) {
+            uint32_t w[4 * N];
+            split_values(code, Lo<T>(0), sh.byte(), sh.byte(), w);
+            store_before(reinterpret_cast<uint16_t*>(y + row + lane * step + ext_col), w, ext_n * H);
+        }
+    }
+    store_scale_tile(staged, scales);   // and, of BOTH, the elements are complete
+    if (BOTH) {
+        uint8_t* const s_codes = smem + kTile * kAnyPitch<T>;
+        uint8_t* const s_scale = s_codes + kTile * kStagePitch;
+        const int warp = threadIdx.x >> 5, blk = warp & 3;
+#pragma unroll 1
+        for (int h = 0; h < 4 * 128 / kRowThreads<T>; ++h) {
+            const int cl = ((warp >> 2) + h * (kRowThreads<T> / 128)) * 32 + (threadIdx.x & 31);
+            Cols<T, 1> v[32];
+            const uint8_t* const from = smem + blk * 32 * kAnyPitch<T> + cl * (int)sizeof(T);
+#pragma unroll
+            for (int t = 0; t < 32; ++t)   // row t of the block starts t * cols elements, modulo a vector, behind a boundary
+                v[t].take(from + t * kAnyPitch<T> + ((t * (cols & (V - 1))) & (V - 1)) * (int)sizeof(T));
+            uint32_t code[1][4];
+            int b[1];
+            Cols<T, 1>::template quantize<32, false>(v, b, code);
+            *reinterpret_cast<uint4*>(s_codes + cl * kStagePitch + blk * 16) = make_uint4(code[0][0], code[0][1], code[0][2], code[0][3]);
+            s_scale[cl * 4 + blk] = (uint8_t)b[0];
+        }
+        store_col_tile(s_codes, s_scale, tile.rt, tile.kt, cols, t_blocks, t_tiles, t_codes, t_scales);
+    }
+}
+
 // Both operands of x in one pass over it: rows as mx4_rows_vec, and the tile
 // through shared memory for the columns, as raw elements in 16-byte chunks.
 // Chunk j of row i lies at j ^ (i & 7) ^ (i & 16 ? 4 : 0): a half warp writes a
@@ -641,7 +688,7 @@ __global__ void __launch_bounds__(kRowThreads<T>, kRowCtas<T>) mx4_both(const T*
             Cols<T, CPT> v[R];
 #pragma unroll
             for (int t = 0; t < R; ++t)
-                v[t].raw = *reinterpret_cast<const decltype(v[t].raw)*>(s_x + chunk_at<T>(row0 + t, cl * (int)sizeof(T) / 16) + cl * sizeof(T) % 16);
+                v[t].take(s_x + chunk_at<T>(row0 + t, cl * (int)sizeof(T) / 16) + cl * sizeof(T) % 16);
             uint32_t code[CPT][R / 8];
             int b[CPT];
             Cols<T, CPT>::template quantize<R, CPT == 2>(v, b, code);
@@ -665,7 +712,9 @@ cudaError_t launch_rows(const T* x, int64_t rows, int cols, uint8_t* codes, uint
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     prof_begin(st);
     if (cols % 8 == 0) mx4_rows_vec<T, DEQ><<<(unsigned)grid, kRowThreads<T>, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y);
-    else mx4_rows_any<T, DEQ><<<(unsigned)grid, kRowThreads<T>, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y);
+    else
+        mx4_rows_any<T, DEQ, false><<<(unsigned)grid, kRowThreads<T>, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y, 0, 0,
+                                                                              nullptr, nullptr);
     prof_end(st, K_MX4_ROWS);
     return cudaGetLastError();
 }
@@ -682,18 +731,24 @@ cudaError_t launch_cols(const T* x, int64_t rows, int cols, uint8_t* codes, uint
     return cudaGetLastError();
 }
 
-// Widths whose rows are not 16-byte aligned take two passes.
 template <typename T>
 cudaError_t launch_both(const T* x, int64_t rows, int cols, uint8_t* codes, uint8_t* scales, uint8_t* t_codes,
                         uint8_t* t_scales, cudaStream_t st) {
-    const int tiles_k = (int)mx4::scale_tiles_k(cols);
-    const int64_t grid = mx4::scale_tiles_r(rows) * tiles_k;
+    const int tiles_k = (int)mx4::scale_tiles_k(cols), pitch = (int)(mx4::padded_cols(cols) / 2);
+    const int64_t grid = mx4::scale_tiles_r(rows) * tiles_k, t_blocks = (rows + 31) / 32, t_tiles = mx4::scale_tiles_k(rows);
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = cudaFuncSetAttribute(mx4_both<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBothSmem<T>);
+    const bool vec = cols % 8 == 0;
+    const cudaError_t e = vec ? cudaFuncSetAttribute(mx4_both<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBothSmem<T>)
+                              : cudaFuncSetAttribute(mx4_rows_any<T, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     kBothAnySmem<T>);
     if (e != cudaSuccess) return e;
     prof_begin(st);
-    mx4_both<T><<<(unsigned)grid, kRowThreads<T>, kBothSmem<T>, st>>>(x, rows, cols, tiles_k, codes, (int)(mx4::padded_cols(cols) / 2),
-                                                                   scales, (rows + 31) / 32, mx4::scale_tiles_k(rows), t_codes, t_scales);
+    if (vec)
+        mx4_both<T><<<(unsigned)grid, kRowThreads<T>, kBothSmem<T>, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, t_blocks,
+                                                                          t_tiles, t_codes, t_scales);
+    else
+        mx4_rows_any<T, false, true><<<(unsigned)grid, kRowThreads<T>, kBothAnySmem<T>, st>>>(
+            x, rows, cols, tiles_k, codes, pitch, scales, nullptr, t_blocks, t_tiles, t_codes, t_scales);
     prof_end(st, K_MX4_BOTH);
     return cudaGetLastError();
 }
@@ -746,15 +801,9 @@ jfa_status quantize_both(const char* who, const void* x, int dtype, int64_t rows
     if (s != JFA_OK || rows == 0 || cols == 0) return s;
     if (!t_codes || !t_scales) return set_last_error(JFA_ERR_INVALID_ARGUMENT, "%s: NULL tensor", who);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (cols % 8 == 0) {
-        e = dtype == JFA_F32 ? launch_both(reinterpret_cast<const float*>(x), rows, (int)cols, codes, scales, t_codes, t_scales, st)
-                             : launch_both(reinterpret_cast<const __nv_bfloat16*>(x), rows, (int)cols, codes, scales, t_codes,
-                                           t_scales, st);
-    } else {
-        e = dispatch<false>(x, dtype, rows, (int)cols, 0, codes, scales, nullptr, st);
-        if (e == cudaSuccess) e = dispatch<false>(x, dtype, rows, (int)cols, 1, t_codes, t_scales, nullptr, st);
-    }
+    const cudaError_t e =
+        dtype == JFA_F32 ? launch_both(reinterpret_cast<const float*>(x), rows, (int)cols, codes, scales, t_codes, t_scales, st)
+                         : launch_both(reinterpret_cast<const __nv_bfloat16*>(x), rows, (int)cols, codes, scales, t_codes, t_scales, st);
     if (e != cudaSuccess) return set_last_error(JFA_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
     return JFA_OK;
 }

@@ -72,6 +72,17 @@ def test_quantise_both_ways_in_one_pass(cuda_device, rows, cols, dtype):
     check_operand(op_t, x, True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 140])
+def test_quantise_both_ways_every_width(cuda_device, dtype, rows):
+    for cols in list(range(1, 20)) + list(range(121, 138)) + [257, 1003]:
+        x = draw(rows, cols, dtype, cols)
+        x[rows // 2, cols // 3] = float("inf")
+        op, op_t = jfa.quantize_mxfp4_both(x.to(cuda_device))
+        check_operand(op, x, False)
+        check_operand(op_t, x, True)
+
+
 @pytest.mark.parametrize("along_rows", [False, True])
 @pytest.mark.parametrize("cols", [256, 131])
 def test_quantise_special_values(cuda_device, along_rows, cols):

@@ -801,18 +801,22 @@ def block_norm_workspace(desc: jfa_block_norm, device) -> torch.Tensor:
 _BLOCK_NORM_PARAMS = ("scale", "post_gamma", "post_beta", "pre_gamma", "pre_beta")
 
 
-def _block_norm_args(desc, x, tensors, params):
-    """Looks the tensors ([rows, dim]) and parameters ([dim] fp32) over; the GPU's index."""
+def _block_norm_args(desc, tensors, params):
+    """Looks the tensors ([rows, dim], the first is x) and parameters ([dim] fp32) over; the GPU's index."""
+    x = tensors[0]
     if not isinstance(x, torch.Tensor):
         _invalid("x: a torch tensor is needed")
-    dim, index, dt = desc.dim, x.get_device(), _JFA_DTYPE.get(desc.dtype, torch.float32)
-    shape, vec = (desc.rows, dim), (dim,)
-    for name, t in zip(("x", "block", "gate", "dy", "dn"), (x,) + tensors):
-        if t is not None and not (_is(t, shape, dt, index) and index >= 0):
-            _refuse(t, name, shape, (dt,), index)
-    for name, t in zip(_BLOCK_NORM_PARAMS, params):
-        if t is not None and not _is(t, vec, torch.float32, index):
-            _refuse(t, name, vec, (torch.float32,), index)
+    dim, index, dt, tensor, f32 = desc.dim, x.get_device(), _JFA_DTYPE.get(desc.dtype, torch.float32), torch.Tensor, torch.float32
+    shape = (desc.rows, dim)
+    for i, t in enumerate(tensors):
+        if t is not None and not (isinstance(t, tensor) and t.shape == shape and t.dtype is dt
+                                  and t.get_device() == index and index >= 0 and t.is_contiguous()):
+            _refuse(t, ("x", "block", "gate", "dy", "dn")[i], shape, (dt,), index)
+    shape = (dim,)
+    for i, t in enumerate(params):
+        if t is not None and not (isinstance(t, tensor) and t.shape == shape and t.dtype is f32
+                                  and t.get_device() == index and t.is_contiguous()):
+            _refuse(t, _BLOCK_NORM_PARAMS[i], shape, (f32,), index)
     return index
 
 
@@ -825,7 +829,7 @@ def block_norm_forward(desc: jfa_block_norm, x, block, gate=None, scale=None, po
     """Allocates and returns (y, n) of jfa_block_norm_forward; n is None
     without a pre_norm."""
     params = (scale, post_gamma, post_beta, pre_gamma, pre_beta)
-    s = _stream_here(_block_norm_args(desc, x, (block, gate), params), stream)
+    s = _stream_here(_block_norm_args(desc, (x, block, gate), params), stream)
     if s is None:
         with _switch(x.device, stream):
             return block_norm_forward(desc, x, block, gate, *params)
@@ -846,7 +850,7 @@ def block_norm_backward(desc: jfa_block_norm, x, block, gate=None, scale=None, p
     with the keys x, block, gate, scale, post_gamma, post_beta, pre_gamma and
     pre_beta (None for an input that is None)."""
     params = (scale, post_gamma, post_beta, pre_gamma, pre_beta)
-    index = _block_norm_args(desc, x, (block, gate, dy, dn), params)
+    index = _block_norm_args(desc, (x, block, gate, dy, dn), params)
     s = _stream_here(index, stream)
     if s is None:
         with _switch(x.device, stream):
@@ -855,10 +859,15 @@ def block_norm_backward(desc: jfa_block_norm, x, block, gate=None, scale=None, p
         ws = block_norm_workspace(desc, x.device)
     elif ws.get_device() != index:
         _invalid(f"ws: device {ws.device}, expected cuda:{index}")
-    g = [torch.empty_like(x), torch.empty_like(x), _like(gate)] + [_like(p) for p in params]
+    dx, dblock, dgate = torch.empty_like(x), torch.empty_like(x), _like(gate)
+    dscale, dpost_gamma, dpost_beta = _like(scale), _like(post_gamma), _like(post_beta)
+    dpre_gamma, dpre_beta = _like(pre_gamma), _like(pre_beta)
     st = (_LIB or load()).jfa_block_norm_backward(
-        ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), *[_ptr(p) for p in params],
-        _ptr(dy), _ptr(dn), *[_ptr(t) for t in g], ws.data_ptr(), ws.numel() * ws.element_size(), s)
+        ctypes.byref(desc), x.data_ptr(), _ptr(block), _ptr(gate), _ptr(scale), _ptr(post_gamma),
+        _ptr(post_beta), _ptr(pre_gamma), _ptr(pre_beta), _ptr(dy), _ptr(dn), dx.data_ptr(),
+        dblock.data_ptr(), _ptr(dgate), _ptr(dscale), _ptr(dpost_gamma), _ptr(dpost_beta),
+        _ptr(dpre_gamma), _ptr(dpre_beta), ws.data_ptr(), ws.numel() * ws.element_size(), s)
     if st:
         _check(st)
-    return dict(zip(("x", "block", "gate") + _BLOCK_NORM_PARAMS, g))
+    return {"x": dx, "block": dblock, "gate": dgate, "scale": dscale, "post_gamma": dpost_gamma,
+            "post_beta": dpost_beta, "pre_gamma": dpre_gamma, "pre_beta": dpre_beta}

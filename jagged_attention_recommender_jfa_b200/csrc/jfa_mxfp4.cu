@@ -124,7 +124,7 @@ template <typename T>
 constexpr int kHalvesOf = kRowThreads<T> / 16;
 template <typename T>
 constexpr int kRowCtas = sizeof(T) == 2 ? 4 : 2;
-// mx4_rows_any, 222283 x 1023 bf16 without / with the copy: 146 / 255 us at 3,
+// mx4_any, 222283 x 1023 bf16 without / with the copy: 146 / 255 us at 3,
 // 140 / 261 at 4 (spills with the copy).
 template <typename T>
 constexpr int kAnyCtas = sizeof(T) == 2 ? 3 : 2;
@@ -380,13 +380,15 @@ struct Cols<float, 1> {
     __device__ static void store(float* p, float a, float) { *p = a; }
 };
 
-// CTAs an SM should hold: one column per thread 2 / 3: 207 / 193 us (222283 x
-// 1023 bf16), two columns 3 / 4: 111 / 117 us without the copy, 214 / 195 with it.
-template <int CPT, bool DEQ>
-constexpr int kColCtas = CPT == 2 && DEQ ? 4 : 3;
+// CTAs an SM should hold, us: fp32 2 / 3 (65537 x 1003) 54 / 58, with the copy
+// 99 / 113 (three spill); bf16, one column per thread, 2 / 3 (222283 x 1023, with
+// the copy) 252 / 246; two columns 3 / 4 / 5 (222283 x 1024) 103 / 93 / 93, with
+// the copy 166 / 167 / 170, a million rows of 100 with it 84 / 78 / 76.
+template <typename T, int CPT>
+constexpr int kColCtas = sizeof(T) == 4 ? 2 : CPT == 2 ? 4 : 3;
 
 template <typename T, int CPT, bool DEQ>
-__global__ void __launch_bounds__(512 / CPT, kColCtas<CPT, DEQ>) mx4_cols(const T* __restrict__ x, int64_t rows, int cols,
+__global__ void __launch_bounds__(512 / CPT, kColCtas<T, CPT>) mx4_cols(const T* __restrict__ x, int64_t rows, int cols,
                                                       int col_tiles, int64_t blocks_k, int64_t tiles_k,
                                                       uint8_t* __restrict__ codes,
                                                       uint8_t* __restrict__ scales, T* __restrict__ y) {
@@ -436,24 +438,25 @@ __global__ void __launch_bounds__(512 / CPT, kColCtas<CPT, DEQ>) mx4_cols(const 
     store_col_tile(s_codes, s_scale, rt, ct, cols, blocks_k, tiles_k, codes, scales);
 }
 
-// BOTH: the operand of the transpose as well; the elements go through shared
-// memory as the vectors hold them, a row of the tile 16 bytes longer than its
-// 128 elements, and a lane then takes 32 rows of a column.  One pass instead of
-// two: 65537 x 1003 bf16 97 -> 68 us, fp32 122 -> 91, 65537 x 4093 bf16 337 ->
-// 240.
+// COLS: the operand of the transpose, alone or as well; the elements go through
+// shared memory as the vectors hold them, a row of the tile 16 bytes longer than
+// its 128 elements, and a lane then takes 32 rows of a column.  Both operands in
+// one pass instead of two: 65537 x 1003 bf16 97 -> 68 us, fp32 122 -> 91, 65537
+// x 4093 bf16 337 -> 240.  Alone, 222283 x 1023 bf16: 123 us, 146 by columns
+// from global memory (mx4_cols, whose fp32 keeps up: 5.5 TB/s).
 template <typename T>
 constexpr int kAnyPitch = kTile * (int)sizeof(T) + 16;
 template <typename T>
-constexpr int kBothAnySmem = kTile * (kAnyPitch<T> + kStagePitch + 4);
+constexpr int kAnySmem = kTile * (kAnyPitch<T> + kStagePitch + 4);
 
-template <typename T, bool DEQ, bool BOTH>
-__global__ void __launch_bounds__(kRowThreads<T>, kAnyCtas<T>) mx4_rows_any(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
+template <typename T, bool ROWS, bool DEQ, bool COLS>
+__global__ void __launch_bounds__(kRowThreads<T>, kAnyCtas<T>) mx4_any(const T* __restrict__ x, int64_t rows, int cols, int tiles_k,
                                                                          uint8_t* __restrict__ codes, int code_pitch,
                                                                          uint8_t* __restrict__ scales, T* __restrict__ y,
                                                                          int64_t t_blocks, int64_t t_tiles,
                                                                          uint8_t* __restrict__ t_codes,
                                                                          uint8_t* __restrict__ t_scales) {
-    extern __shared__ __align__(16) uint8_t smem[];   // BOTH: elements, codes and scales of the columns
+    extern __shared__ __align__(16) uint8_t smem[];   // COLS: elements, codes and scales of the columns
     constexpr int kHalves = kHalvesOf<T>, kSegs = 128 / kHalves;
     constexpr int V = 16 / sizeof(T), N = 8 / V, H = sizeof(T) / 2;   // elements of a vector, vectors of eight, half words
     __shared__ __align__(16) uint8_t staged[512];
@@ -528,7 +531,8 @@ __global__ void __launch_bounds__(kRowThreads<T>, kAnyCtas<T>) mx4_rows_any(cons
 #pragma unroll
     for (int i = 0; i < kSegs; ++i) {
         if (c + 8 > cols) raw[i].clip(cols - c);   // the rest is the next row's
-        if (BOTH) raw[i].put_vectors(smem + (i * kHalves + half) * kAnyPitch<T> + lane * 8 * (int)sizeof(T));
+        if (COLS) raw[i].put_vectors(smem + (i * kHalves + half) * kAnyPitch<T> + lane * 8 * (int)sizeof(T));
+        if (!ROWS) continue;
         uint32_t m_lo, m;
         max_split(raw[i], lo, m_lo, m);
         const uint32_t behind = __shfl_down_sync(0xffffffffu, m_lo, 1, 16), last = __shfl_sync(0xffffffffu, ext_max, i, 16);
@@ -577,9 +581,9 @@ __global__ void __launch_bounds__(kRowThreads<T>, kAnyCtas<T>) mx4_rows_any(cons
             o += step;
         }
     }
-    if (BOTH && lane < kSegs) ext.put_vector(smem + (lane * kHalves + half) * kAnyPitch<T> + kTile * (int)sizeof(T));
+    if (COLS && lane < kSegs) ext.put_vector(smem + (lane * kHalves + half) * kAnyPitch<T> + kTile * (int)sizeof(T));
     // the rows' last lanes: their codes with the ones behind, and the values of those
-    if (lane < kSegs && lane * kHalves < left) {
+    if (ROWS && lane < kSegs && lane * kHalves < left) {
         const Shared sh(ext_m);
         const uint32_t code = ext.codes(sh);
         if (c0 + 120 < 2 * code_pitch)
@@ -591,8 +595,9 @@ __global__ void __launch_bounds__(kRowThreads<T>, kAnyCtas<T>) mx4_rows_any(cons
             store_before(reinterpret_cast<uint16_t*>(y + row + lane * step + ext_col), w, ext_n * H);
         }
     }
-    store_scale_tile(staged, scales);   // and, of BOTH, the elements are complete
-    if (BOTH) {
+    if (ROWS) store_scale_tile(staged, scales);
+    if (COLS) {
+        __syncthreads();   // the elements are complete
         uint8_t* const s_codes = smem + kTile * kAnyPitch<T>;
         uint8_t* const s_scale = s_codes + kTile * kStagePitch;
         const int warp = threadIdx.x >> 5, blk = warp & 3;
@@ -713,8 +718,8 @@ cudaError_t launch_rows(const T* x, int64_t rows, int cols, uint8_t* codes, uint
     prof_begin(st);
     if (cols % 8 == 0) mx4_rows_vec<T, DEQ><<<(unsigned)grid, kRowThreads<T>, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y);
     else
-        mx4_rows_any<T, DEQ, false><<<(unsigned)grid, kRowThreads<T>, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y, 0, 0,
-                                                                              nullptr, nullptr);
+        mx4_any<T, true, DEQ, false><<<(unsigned)grid, kRowThreads<T>, 0, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, y, 0, 0,
+                                                                                nullptr, nullptr);
     prof_end(st, K_MX4_ROWS);
     return cudaGetLastError();
 }
@@ -739,22 +744,38 @@ cudaError_t launch_both(const T* x, int64_t rows, int cols, uint8_t* codes, uint
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const bool vec = cols % 8 == 0;
     const cudaError_t e = vec ? cudaFuncSetAttribute(mx4_both<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBothSmem<T>)
-                              : cudaFuncSetAttribute(mx4_rows_any<T, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     kBothAnySmem<T>);
+                              : cudaFuncSetAttribute(mx4_any<T, true, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     kAnySmem<T>);
     if (e != cudaSuccess) return e;
     prof_begin(st);
     if (vec)
         mx4_both<T><<<(unsigned)grid, kRowThreads<T>, kBothSmem<T>, st>>>(x, rows, cols, tiles_k, codes, pitch, scales, t_blocks,
                                                                           t_tiles, t_codes, t_scales);
     else
-        mx4_rows_any<T, false, true><<<(unsigned)grid, kRowThreads<T>, kBothAnySmem<T>, st>>>(
+        mx4_any<T, true, false, true><<<(unsigned)grid, kRowThreads<T>, kAnySmem<T>, st>>>(
             x, rows, cols, tiles_k, codes, pitch, scales, nullptr, t_blocks, t_tiles, t_codes, t_scales);
     prof_end(st, K_MX4_BOTH);
     return cudaGetLastError();
 }
 
+// The operand of the transpose of a bf16 x of odd width, without the copy.
+cudaError_t launch_cols_odd(const __nv_bfloat16* x, int64_t rows, int cols, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+    using T = __nv_bfloat16;
+    const int tiles_k = (int)mx4::scale_tiles_k(cols);
+    const int64_t grid = mx4::scale_tiles_r(rows) * tiles_k;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = cudaFuncSetAttribute(mx4_any<T, false, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAnySmem<T>);
+    if (e != cudaSuccess) return e;
+    prof_begin(st);
+    mx4_any<T, false, false, true><<<(unsigned)grid, kRowThreads<T>, kAnySmem<T>, st>>>(
+        x, rows, cols, tiles_k, nullptr, 0, nullptr, nullptr, (rows + 31) / 32, mx4::scale_tiles_k(rows), codes, scales);
+    prof_end(st, K_MX4_COLS);
+    return cudaGetLastError();
+}
+
 // A bf16 row of an even width is 4-byte aligned, so its columns can be taken
-// in pairs; other widths take one column per thread.
+// in pairs; an odd width's go through shared memory or, with the copy, which is
+// written by columns too, one by one.
 template <bool DEQ>
 cudaError_t dispatch(const void* x, int dtype, int64_t rows, int cols, int along_rows, uint8_t* codes,
                      uint8_t* scales, void* y, cudaStream_t st) {
@@ -767,8 +788,9 @@ cudaError_t dispatch(const void* x, int dtype, int64_t rows, int cols, int along
     const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(x);
     __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(y);
     if (!along_rows) return launch_rows<__nv_bfloat16, DEQ>(p, rows, cols, codes, scales, o, st);
-    return cols % 2 == 0 ? launch_cols<__nv_bfloat16, 2, DEQ>(p, rows, cols, codes, scales, o, st)
-                         : launch_cols<__nv_bfloat16, 1, DEQ>(p, rows, cols, codes, scales, o, st);
+    if (cols % 2 == 0) return launch_cols<__nv_bfloat16, 2, DEQ>(p, rows, cols, codes, scales, o, st);
+    if constexpr (DEQ) return launch_cols<__nv_bfloat16, 1, true>(p, rows, cols, codes, scales, o, st);
+    else return launch_cols_odd(p, rows, cols, codes, scales, st);
 }
 
 jfa_status check_quantize(const char* who, const void* x, int dtype, int64_t rows, int64_t cols, const uint8_t* codes,

@@ -397,9 +397,15 @@ constexpr int kFwdBound = NCH > 1 ? (sizeof(T) == 4 && NCH == 2 ? 640 : kMaxThre
 template <typename T, int NCH>
 constexpr int kBwdBound = NCH == 1 && sizeof(T) == 4 ? 768 : kMaxThreads;
 
+// bf16 rows of two vectors per thread spill at 128 registers; up to 384 threads
+// (6144 columns) there are 168.
+constexpr int kFewThreads = 384;
+template <typename T, int BOUND>
+constexpr int kTwoBound = sizeof(T) == 2 ? kFewThreads : BOUND;
+
 // LN: a norm is a LayerNorm, so that there may be betas.
-template <typename T, int NCH, bool LN>
-__global__ void __launch_bounds__(kFwdBound<T, NCH>) block_norm_fwd(const NormArgs a, int G) {
+template <typename T, int NCH, bool LN, int BOUND = kFwdBound<T, NCH>>
+__global__ void __launch_bounds__(BOUND, 1) block_norm_fwd(const NormArgs a, int G) {
     constexpr int P = Cols<T, NCH>::P;
     extern __shared__ float4 smem4[];
     __shared__ GroupBuf buf;
@@ -493,8 +499,8 @@ struct Sums<P, Q, true> {
     __device__ __forceinline__ float2 get(int q, int i) const { return mine[(q * P + i) * stride]; }
 };
 
-template <typename T, int NCH, bool LN>
-__global__ void __launch_bounds__(kBwdBound<T, NCH>) block_norm_bwd(const NormArgs a, int G) {
+template <typename T, int NCH, bool LN, int BOUND = kBwdBound<T, NCH>>
+__global__ void __launch_bounds__(BOUND, 1) block_norm_bwd(const NormArgs a, int G) {
     constexpr int V = Vec<T>::N, P = Cols<T, NCH>::P, Q = LN ? 4 : 2;
     constexpr bool kSmem = kSumsInSmem<T, NCH, LN>, kAhead = NCH == 1;
     extern __shared__ float4 smem4[];   // parameters, sums, each where they are kept here; at the end the small groups' reduction
@@ -707,7 +713,7 @@ RowShape row_shape(int D) {
     RowShape s{};
     const int vecs = D % V == 0 ? D / V : (D + V - 2) / V + 1;
     const int one = sizeof(T) == 2 ? kMaxThreads : (LN ? 128 : 384);   // most vectors of a row with one per thread
-    s.nch = vecs <= one ? 1 : (vecs <= 2 * kMaxThreads ? 2 : kMostChunks<T>);
+    s.nch = vecs <= one ? 1 : (vecs <= 2 * kMaxThreads ? 2 : (vecs + kMaxThreads - 1) / kMaxThreads);
     const int need = (vecs + s.nch - 1) / s.nch;
     if (need > 32) {
         s.G = (need + 31) / 32 * 32;
@@ -783,9 +789,12 @@ cudaError_t allow_smem(K kern, size_t smem) {
 template <typename T, bool LN>
 cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
     const RowShape s = row_shape<T, LN>(a.D);
+    constexpr int M = kMostChunks<T>;
     void (*kern)(NormArgs, int) = s.nch == 1   ? block_norm_fwd<T, 1, LN>
-                                  : s.nch == 2 ? block_norm_fwd<T, 2, LN>
-                                               : block_norm_fwd<T, kMostChunks<T>, LN>;
+                                  : s.nch == 2 ? (s.threads <= kFewThreads ? block_norm_fwd<T, 2, LN, kTwoBound<T, kFwdBound<T, 2>>> : block_norm_fwd<T, 2, LN>)
+                                  : s.nch == 3 ? block_norm_fwd<T, 3, LN>
+                                  : s.nch == 4 ? block_norm_fwd<T, M < 4 ? M : 4, LN>
+                                               : block_norm_fwd<T, M, LN>;
     const bool in_smem_par = s.nch == 1 || (s.nch == 2 && kParamsInSmem<T, 2>);
     const size_t smem = in_smem_par ? s.nch * Params<LN ? 4 : 2, Vec<T>::N / 2, true>::bytes(s.threads) : 0;
     int grid = 0;
@@ -803,9 +812,12 @@ template <typename T, bool LN>
 cudaError_t bwd_launch(const NormArgs& a, int* parts, cudaStream_t st) {
     const RowShape s = row_shape<T, LN>(a.D);
     constexpr int Q = LN ? 4 : 2;
+    constexpr int M = kMostChunks<T>;
     void (*kern)(NormArgs, int) = s.nch == 1   ? block_norm_bwd<T, 1, LN>
-                                  : s.nch == 2 ? block_norm_bwd<T, 2, LN>
-                                               : block_norm_bwd<T, kMostChunks<T>, LN>;
+                                  : s.nch == 2 ? (s.threads <= kFewThreads ? block_norm_bwd<T, 2, LN, kTwoBound<T, kBwdBound<T, 2>>> : block_norm_bwd<T, 2, LN>)
+                                  : s.nch == 3 ? block_norm_bwd<T, 3, LN>
+                                  : s.nch == 4 ? block_norm_bwd<T, M < 4 ? M : 4, LN>
+                                               : block_norm_bwd<T, M, LN>;
     const int pairs = s.nch * Vec<T>::N / 2;
     const bool in_smem_par = s.nch == 1 || (s.nch == 2 && kParamsInSmem<T, 2>);
     const bool in_smem = s.nch == 1 ? kSumsInSmem<T, 1, LN> : (s.nch == 2 ? kSumsInSmem<T, 2, LN> : true);

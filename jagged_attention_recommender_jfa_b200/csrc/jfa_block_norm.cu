@@ -229,10 +229,12 @@ struct Cols {
     }
 };
 
-// A thread's parameters, K vectors of P pairs.  With up to eight elements per
-// thread and tensor (MEM) they wait in shared memory, each thread its own:
-// registers are what limits the warps of an SM there, and those hide the
-// latencies of the row sums.  Wider rows keep them in registers.
+// A thread's parameters, K vectors of P pairs.  Where they fit beside the sums
+// (MEM) they wait in shared memory, each thread its own: registers are what
+// limits the warps of an SM with up to eight elements per thread and tensor, and
+// those hide the latencies of the row sums; and what spills in wide rows (us in
+// registers / in shared memory: 10000 x 8192 fp32 RMS forward 356 / 320,
+// backward 733 / 671, 15000 x 6000 bf16 LayerNorm 402 / 355 and 769 / 802).
 template <int K, int P, bool MEM>
 struct Params {
     float2 v[K][P];
@@ -258,7 +260,6 @@ struct Params<K, P, true> {
             f[i + 1] = make_float2(q.z, q.w);
         }
     }
-    static constexpr size_t bytes(int threads) { return sizeof(float2) * K * P * threads; }
 };
 
 // 1 / (1 + e^-u) with the hardware's base-2 exponential and reciprocal (a few
@@ -383,8 +384,9 @@ __device__ __forceinline__ float to_y(const Par& par, int W1, int W0, int post, 
     return r;
 }
 
-template <typename T, int NCH>
-constexpr bool kParamsInSmem = NCH * Vec<T>::N <= 8;
+// Whether so many vectors of a thread's pairs fit into shared memory.
+template <typename T, int NCH, int VECTORS, int BOUND>
+constexpr bool kFits = VECTORS * (NCH * Vec<T>::N / 2) * (int)sizeof(float2) * BOUND <= 220 * 1024;
 
 // Registers per thread through the launch bound: 80 for the forward (64 fp32,
 // 96 with two vectors)
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(BOUND, 1) block_norm_fwd(const NormArgs a, int
     extern __shared__ float4 smem4[];
     __shared__ GroupBuf buf;
     Group g(G, &buf);
-    Params<LN ? 4 : 2, P, kParamsInSmem<T, NCH>> par(reinterpret_cast<float*>(smem4));
+    Params<LN ? 4 : 2, P, kFits<T, NCH, LN ? 4 : 2, BOUND>> par(reinterpret_cast<float*>(smem4));
     const int groups = blockDim.x / G;
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t base = (int64_t)blockIdx.x * groups, row = base + threadIdx.x / G;
@@ -468,6 +470,8 @@ template <typename T, int NCH, bool LN>
 constexpr bool kSumsInSmem = NCH * Vec<T>::N > 8 || LN;
 template <bool LN>
 constexpr int kBwdParams = LN ? 3 : 2;
+template <typename T, int NCH, bool LN, int BOUND>
+constexpr bool kBwdParamsInSmem = kFits<T, NCH, kBwdParams<LN> + (kSumsInSmem<T, NCH, LN> ? (LN ? 4 : 2) : 0), BOUND>;
 template <int P, int Q, bool SMEM>
 struct Sums {
     float2 v[Q][P];
@@ -507,8 +511,9 @@ __global__ void __launch_bounds__(BOUND, 1) block_norm_bwd(const NormArgs a, int
     float* const smem = reinterpret_cast<float*>(smem4);
     __shared__ GroupBuf buf;
     Group g(G, &buf);
-    Params<kBwdParams<LN>, P, kParamsInSmem<T, NCH>> par(smem);
-    Sums<P, Q, kSmem> sums(smem + (kParamsInSmem<T, NCH> ? kBwdParams<LN> * 2 * P * blockDim.x : 0));
+    constexpr bool kPar = kBwdParamsInSmem<T, NCH, LN, BOUND>;
+    Params<kBwdParams<LN>, P, kPar> par(smem);
+    Sums<P, Q, kSmem> sums(smem + (kPar ? kBwdParams<LN> * 2 * P * blockDim.x : 0));
     const int groups = blockDim.x / G;
     const int64_t stride = (int64_t)gridDim.x * groups;
     int64_t base = (int64_t)blockIdx.x * groups, row = base + threadIdx.x / G;
@@ -629,7 +634,7 @@ __global__ void __launch_bounds__(BOUND, 1) block_norm_bwd(const NormArgs a, int
     } else {
         // the groups' sums in group order, through shared memory [groups][D]
         // behind the parameters and sums
-        float* const area = smem + ((kParamsInSmem<T, NCH> ? kBwdParams<LN> : 0) + (kSmem ? Q : 0)) * 2 * P * blockDim.x;
+        float* const area = smem + ((kPar ? kBwdParams<LN> : 0) + (kSmem ? Q : 0)) * 2 * P * blockDim.x;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             __syncthreads();
@@ -701,7 +706,9 @@ struct RowShape {
     int period;   // rows after which the alignment repeats
 };
 // Vectors per thread of the widest rows: 8191 columns that start off a
-// boundary take 1025 vectors of bf16 and 2049 of fp32.
+// boundary take 1025 vectors of bf16 and 2049 of fp32.  Above 2 x 512 vectors
+// each count has its kernels (10000 x 6731 fp32 LayerNorm-free backward: 1617 us
+// as one of five, for which the compiler then took 64 registers, 689 as four).
 template <typename T>
 constexpr int kMostChunks = sizeof(T) == 4 ? 5 : 3;
 static_assert(kMostChunks<float> * kMaxThreads * 4 >= kMaxDim + 4 && kMostChunks<__nv_bfloat16> * kMaxThreads * 8 >= kMaxDim + 8,
@@ -786,23 +793,55 @@ cudaError_t allow_smem(K kern, size_t smem) {
     return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
 }
 
+// A kernel and the vectors of its threads' pairs that it keeps in shared memory.
+struct Kernel {
+    void (*kern)(NormArgs, int);
+    int vectors;
+};
+template <typename T, int NCH, bool LN, int BOUND = kFwdBound<T, NCH>>
+Kernel fwd_kernel() {
+    return {block_norm_fwd<T, NCH, LN, BOUND>, kFits<T, NCH, LN ? 4 : 2, BOUND> ? (LN ? 4 : 2) : 0};
+}
+template <typename T, int NCH, bool LN, int BOUND = kBwdBound<T, NCH>>
+Kernel bwd_kernel() {
+    return {block_norm_bwd<T, NCH, LN, BOUND>,
+            (kBwdParamsInSmem<T, NCH, LN, BOUND> ? kBwdParams<LN> : 0) + (kSumsInSmem<T, NCH, LN> ? (LN ? 4 : 2) : 0)};
+}
+// bf16 rows have at most three vectors per thread.
+template <typename T, bool LN>
+Kernel fwd_kernel_of(const RowShape& s) {
+    constexpr int M = kMostChunks<T>;
+    switch (s.nch) {
+        case 1: return fwd_kernel<T, 1, LN>();
+        case 2: return s.threads <= kFewThreads ? fwd_kernel<T, 2, LN, kTwoBound<T, kFwdBound<T, 2>>>() : fwd_kernel<T, 2, LN>();
+        case 3: return fwd_kernel<T, 3, LN>();
+        case 4: return fwd_kernel<T, M < 4 ? M : 4, LN>();
+        default: return fwd_kernel<T, M, LN>();
+    }
+}
+template <typename T, bool LN>
+Kernel bwd_kernel_of(const RowShape& s) {
+    constexpr int M = kMostChunks<T>;
+    switch (s.nch) {
+        case 1: return bwd_kernel<T, 1, LN>();
+        case 2: return s.threads <= kFewThreads ? bwd_kernel<T, 2, LN, kTwoBound<T, kBwdBound<T, 2>>>() : bwd_kernel<T, 2, LN>();
+        case 3: return bwd_kernel<T, 3, LN>();
+        case 4: return bwd_kernel<T, M < 4 ? M : 4, LN>();
+        default: return bwd_kernel<T, M, LN>();
+    }
+}
+
 template <typename T, bool LN>
 cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
     const RowShape s = row_shape<T, LN>(a.D);
-    constexpr int M = kMostChunks<T>;
-    void (*kern)(NormArgs, int) = s.nch == 1   ? block_norm_fwd<T, 1, LN>
-                                  : s.nch == 2 ? (s.threads <= kFewThreads ? block_norm_fwd<T, 2, LN, kTwoBound<T, kFwdBound<T, 2>>> : block_norm_fwd<T, 2, LN>)
-                                  : s.nch == 3 ? block_norm_fwd<T, 3, LN>
-                                  : s.nch == 4 ? block_norm_fwd<T, M < 4 ? M : 4, LN>
-                                               : block_norm_fwd<T, M, LN>;
-    const bool in_smem_par = s.nch == 1 || (s.nch == 2 && kParamsInSmem<T, 2>);
-    const size_t smem = in_smem_par ? s.nch * Params<LN ? 4 : 2, Vec<T>::N / 2, true>::bytes(s.threads) : 0;
+    const Kernel k = fwd_kernel_of<T, LN>(s);
+    const size_t smem = sizeof(float2) * (s.nch * Vec<T>::N / 2) * s.threads * k.vectors;
     int grid = 0;
-    cudaError_t e = allow_smem(kern, smem);
-    if (e == cudaSuccess) e = row_grid(kern, s, a.rows, smem, 0x7fffffff, &grid);
+    cudaError_t e = allow_smem(k.kern, smem);
+    if (e == cudaSuccess) e = row_grid(k.kern, s, a.rows, smem, 0x7fffffff, &grid);
     if (e != cudaSuccess) return e;
     prof_begin(st);
-    kern<<<grid, s.threads, smem, st>>>(a, s.G);
+    k.kern<<<grid, s.threads, smem, st>>>(a, s.G);
     prof_end(st, K_BLOCK_NORM_FWD);
     return cudaGetLastError();
 }
@@ -811,23 +850,14 @@ cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
 template <typename T, bool LN>
 cudaError_t bwd_launch(const NormArgs& a, int* parts, cudaStream_t st) {
     const RowShape s = row_shape<T, LN>(a.D);
-    constexpr int Q = LN ? 4 : 2;
-    constexpr int M = kMostChunks<T>;
-    void (*kern)(NormArgs, int) = s.nch == 1   ? block_norm_bwd<T, 1, LN>
-                                  : s.nch == 2 ? (s.threads <= kFewThreads ? block_norm_bwd<T, 2, LN, kTwoBound<T, kBwdBound<T, 2>>> : block_norm_bwd<T, 2, LN>)
-                                  : s.nch == 3 ? block_norm_bwd<T, 3, LN>
-                                  : s.nch == 4 ? block_norm_bwd<T, M < 4 ? M : 4, LN>
-                                               : block_norm_bwd<T, M, LN>;
-    const int pairs = s.nch * Vec<T>::N / 2;
-    const bool in_smem_par = s.nch == 1 || (s.nch == 2 && kParamsInSmem<T, 2>);
-    const bool in_smem = s.nch == 1 ? kSumsInSmem<T, 1, LN> : (s.nch == 2 ? kSumsInSmem<T, 2, LN> : true);
-    const size_t smem = sizeof(float2) * pairs * s.threads * ((in_smem_par ? kBwdParams<LN> : 0) + (in_smem ? Q : 0)) +
+    const Kernel k = bwd_kernel_of<T, LN>(s);
+    const size_t smem = sizeof(float2) * (s.nch * Vec<T>::N / 2) * s.threads * k.vectors +
                         (s.groups > 1 ? sizeof(float) * s.groups * a.D : 0);
-    cudaError_t e = allow_smem(kern, smem);
-    if (e == cudaSuccess) e = row_grid(kern, s, a.rows, smem, kMaxParts, parts);
+    cudaError_t e = allow_smem(k.kern, smem);
+    if (e == cudaSuccess) e = row_grid(k.kern, s, a.rows, smem, kMaxParts, parts);
     if (e != cudaSuccess) return e;
     prof_begin(st);
-    kern<<<*parts, s.threads, smem, st>>>(a, s.G);
+    k.kern<<<*parts, s.threads, smem, st>>>(a, s.G);
     prof_end(st, K_BLOCK_NORM_BWD);
     return cudaGetLastError();
 }

@@ -96,6 +96,15 @@ def test_sizes(cuda_device, rows, dim, dtype, kind):
     check(cuda_device, rows, dim, dtype, kind, kind, "silu", seed=rows + dim)
 
 
+# every count of vectors per thread and both register budgets of wide rows, with
+# rows that go round and, in the odd widths, start off the boundaries
+@pytest.mark.parametrize("rows,dim", [(310, 4500), (3, 5003), (2, 6144), (310, 6731), (4, 6152), (301, 8185)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("post,pre,gate", [("rms", "rms", "silu"), ("layer", "layer", "sigmoid"), ("none", "layer", "none")])
+def test_wide_rows(cuda_device, rows, dim, dtype, post, pre, gate):
+    check(cuda_device, rows, dim, dtype, post, pre, gate, seed=dim)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_without_parameters(cuda_device, dtype):
     check(cuda_device, 65, 200, dtype, "layer", "rms", "sigmoid", params=False)

@@ -707,8 +707,8 @@ struct RowShape {
 };
 // Vectors per thread of the widest rows: 8191 columns that start off a
 // boundary take 1025 vectors of bf16 and 2049 of fp32.  Above 2 x 512 vectors
-// each count has its kernels (10000 x 6731 fp32 LayerNorm-free backward: 1617 us
-// as one of five, for which the compiler then took 64 registers, 689 as four).
+// each count has its kernels (10000 x 6731 fp32 RMS backward: 1617 us with five
+// vectors, for which the compiler took 64 registers, 689 with four).
 template <typename T>
 constexpr int kMostChunks = sizeof(T) == 4 ? 5 : 3;
 static_assert(kMostChunks<float> * kMaxThreads * 4 >= kMaxDim + 4 && kMostChunks<__nv_bfloat16> * kMaxThreads * 8 >= kMaxDim + 8,

@@ -787,25 +787,45 @@ jfa_status check_params(const jfa_block_norm* d, const void* gate, const float* 
     return JFA_OK;
 }
 
-template <typename K>
-cudaError_t allow_smem(K kern, size_t smem) {
-    // 48 KB, static shared memory included, need no permission
-    return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
-}
-
-// A kernel and the vectors of its threads' pairs that it keeps in shared memory.
+// A kernel, the vectors of its threads' pairs that it keeps in shared memory and
+// the most shared memory that a call of any of its widths asks for.  That
+// constant, and not the call's own need, is the limit that is set: the limit
+// belongs to the device, so that a narrow call of another host thread would
+// otherwise lower it between a wide call's setting and its launch.
 struct Kernel {
     void (*kern)(NormArgs, int);
     int vectors;
+    size_t most;
 };
+// `vectors` of up to BOUND threads, or of the CTAs of several rows with the
+// area that these sum their groups in (at most their threads' columns).
+template <typename T, int NCH, int BOUND>
+constexpr size_t most_smem(int vectors) {
+    const size_t each = sizeof(float2) * (NCH * Vec<T>::N / 2) * vectors;
+    const size_t wide = each * (BOUND < kMaxThreads ? BOUND : kMaxThreads);
+    const size_t small = (each + sizeof(float) * NCH * Vec<T>::N) * kSmallThreads;
+    return wide > small ? wide : small;
+}
+constexpr size_t kSmemOfSm = 227 * 1024;
+
+cudaError_t allow_smem(const Kernel& k, size_t smem) {
+    // 48 KB, static shared memory included, need no permission
+    return smem > 40 * 1024 ? cudaFuncSetAttribute(k.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.most) : cudaSuccess;
+}
+
 template <typename T, int NCH, bool LN, int BOUND = kFwdBound<T, NCH>>
 Kernel fwd_kernel() {
-    return {block_norm_fwd<T, NCH, LN, BOUND>, kFits<T, NCH, LN ? 4 : 2, BOUND> ? (LN ? 4 : 2) : 0};
+    constexpr int vectors = kFits<T, NCH, LN ? 4 : 2, BOUND> ? (LN ? 4 : 2) : 0;
+    constexpr size_t most = most_smem<T, NCH, BOUND>(vectors);
+    static_assert(most + sizeof(GroupBuf) <= kSmemOfSm, "shared memory");
+    return {block_norm_fwd<T, NCH, LN, BOUND>, vectors, most};
 }
 template <typename T, int NCH, bool LN, int BOUND = kBwdBound<T, NCH>>
 Kernel bwd_kernel() {
-    return {block_norm_bwd<T, NCH, LN, BOUND>,
-            (kBwdParamsInSmem<T, NCH, LN, BOUND> ? kBwdParams<LN> : 0) + (kSumsInSmem<T, NCH, LN> ? (LN ? 4 : 2) : 0)};
+    constexpr int vectors = (kBwdParamsInSmem<T, NCH, LN, BOUND> ? kBwdParams<LN> : 0) + (kSumsInSmem<T, NCH, LN> ? (LN ? 4 : 2) : 0);
+    constexpr size_t most = most_smem<T, NCH, BOUND>(vectors);
+    static_assert(most + sizeof(GroupBuf) <= kSmemOfSm, "shared memory");
+    return {block_norm_bwd<T, NCH, LN, BOUND>, vectors, most};
 }
 // bf16 rows have at most three vectors per thread.
 template <typename T, bool LN>
@@ -837,7 +857,7 @@ cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
     const Kernel k = fwd_kernel_of<T, LN>(s);
     const size_t smem = sizeof(float2) * (s.nch * Vec<T>::N / 2) * s.threads * k.vectors;
     int grid = 0;
-    cudaError_t e = allow_smem(k.kern, smem);
+    cudaError_t e = allow_smem(k, smem);
     if (e == cudaSuccess) e = row_grid(k.kern, s, a.rows, smem, 0x7fffffff, &grid);
     if (e != cudaSuccess) return e;
     prof_begin(st);
@@ -853,7 +873,7 @@ cudaError_t bwd_launch(const NormArgs& a, int* parts, cudaStream_t st) {
     const Kernel k = bwd_kernel_of<T, LN>(s);
     const size_t smem = sizeof(float2) * (s.nch * Vec<T>::N / 2) * s.threads * k.vectors +
                         (s.groups > 1 ? sizeof(float) * s.groups * a.D : 0);
-    cudaError_t e = allow_smem(k.kern, smem);
+    cudaError_t e = allow_smem(k, smem);
     if (e == cudaSuccess) e = row_grid(k.kern, s, a.rows, smem, kMaxParts, parts);
     if (e != cudaSuccess) return e;
     prof_begin(st);

@@ -338,6 +338,14 @@ __device__ __forceinline__ void scale_shift(const Par& par, int k1, int k0, floa
     }
 }
 
+// sum / D, corrected to the last place: exact for a row of one number whose sum
+// is exact (the rounding of 1 / D alone left 6e-8 of the number, which 1 /
+// sqrt(eps) makes 0.02 at 1000).
+__device__ __forceinline__ float mean_of(float sum, int D, float inv_d) {
+    const float mu = sum * inv_d;
+    return fmaf(fmaf(-mu, (float)D, sum), inv_d, mu);
+}
+
 // The block's norm and the way to y.  In: b, x, k = act(u) (ones without a
 // gate).  Out: b = hat of the block, x = y - mu_y with mu_y the mean for a
 // LayerNorm next and 0 otherwise; returns the block's r.  The mean of
@@ -352,9 +360,7 @@ __device__ __forceinline__ float to_y(const Par& par, int W1, int W0, int post, 
     if (LN && post == JFA_NORM_LAYER) {
         float s[1] = {plain_sum<P>(b)};
         g.template sum<1>(s);
-        // s / D, corrected to the last place: exact for a constant row of exact sum
-        const float mu = s[0] * inv_d;
-        shift_by<P>(b, -fmaf(fmaf(-mu, (float)cols.D, s[0]), inv_d, mu));
+        shift_by<P>(b, -mean_of(s[0], cols.D, inv_d));
         cols.mask(b);
     }
     float2 w[P];
@@ -372,7 +378,7 @@ __device__ __forceinline__ float to_y(const Par& par, int W1, int W0, int post, 
         float s[3] = {dot<P>(b, b), plain_sum<P>(x), plain_sum<P>(w)};
         g.template sum<3>(s);
         if (post != JFA_NORM_NONE) r = rsqrtf(fmaf(s[0], inv_d, eps));
-        mu_y = fmaf(r, s[2], s[1]) * inv_d;
+        mu_y = mean_of(fmaf(r, s[2], s[1]), cols.D, inv_d);
     } else if (post != JFA_NORM_NONE) {
         float s[1] = {dot<P>(b, b)};
         g.template sum<1>(s);

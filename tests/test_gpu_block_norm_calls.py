@@ -1,13 +1,14 @@
-"""Calls of the block norms on the GPU from host threads side by side."""
+"""The block norms on the GPU: host threads side by side, rows of one number."""
 import ctypes
 import sys
 import threading
 
+import numpy as np
 import pytest
 import torch
 
 from jagged_attention_recommender_jfa_b200 import jfa
-from test_gpu_block_norm import dev_, make
+from test_gpu_block_norm import TORCH, dev_, make
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,23 @@ def test_host_threads_with_widths_of_one_kernel(cuda_device, dtype, narrow, wide
     for _, status, want, got, _ in callers:
         assert len(status) == 1500 and not any(status), (sum(map(bool, status)), max(status))
         assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,value", [(1000, 1000.0), (1003, 24.0), (48, -7.0), (5000, 512.0), (7, 3.0)])
+def test_constant_stream_is_centred_to_zero(cuda_device, dtype, dim, value):
+    # y is one number throughout a row and its sums are whole numbers below
+    # 2^24, so its mean is exact: n is beta and dgamma zero, whatever 1 / D rounds to
+    x = torch.full((5, dim), value, dtype=TORCH[dtype], device=cuda_device)
+    zero = torch.zeros_like(x)
+    up = torch.from_numpy(np.random.default_rng(dim).normal(size=(5, dim))).to(x)
+    beta = torch.arange(dim, dtype=torch.float32, device=cuda_device)
+    gamma = torch.full_like(beta, 2.0)
+    assert abs(value) * dim < 2 ** 24
+    for post in ("none", "rms", "layer"):
+        desc = jfa.make_block_norm(rows=5, dim=dim, dtype=dtype, post_norm=post, pre_norm="layer", gate="none", eps=1e-6)
+        y, n = jfa.block_norm_forward(desc, x, zero, pre_gamma=gamma, pre_beta=beta)
+        assert torch.equal(y, x)
+        assert torch.equal(n, beta.to(x.dtype).expand(5, dim)), (post, (n - beta).abs().max())
+        g = jfa.block_norm_backward(desc, x, zero, pre_gamma=gamma, pre_beta=beta, dy=up, dn=up)
+        assert (g["pre_gamma"] == 0).all(), post

@@ -678,6 +678,13 @@ def _vector(t, name, n, index):
         _refuse(t, name, (n,), (torch.float32,), index)
 
 
+def _readable(ws, check):
+    """Refuses a call whose error word nobody could read: not read here, and in
+    a workspace that is gone when the call returns."""
+    if ws is None and not check:
+        _invalid("check=False needs ws, whose error word jfa_check_error(ws) reads later")
+
+
 def _ws_on(ws, index):
     """The caller's workspace, on the GPU, or a fresh one."""
     if ws is None:
@@ -692,7 +699,9 @@ def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torc
     """``a`` [m, k] times the transpose of ``b`` [n, k] (+ ``bias`` [n] fp32),
     allocated in ``out_dtype`` unless ``out`` is given; ``accumulate`` adds to
     ``out``.  ``ws``: :func:`mxfp4_workspace`; ``check`` as in
-    :func:`attention_forward`."""
+    :func:`attention_forward`, and ``check=False`` (what a captured call needs)
+    only with ``ws``."""
+    _readable(ws, check)
     a_codes, a_scales, m, k = _operand(a, "a")
     index = a_codes.get_device()
     b_codes, b_scales, n, kb = _operand(b, "b", index)
@@ -726,7 +735,9 @@ def matmul_mxfp4(a: MxOperand, b: MxOperand, bias=None, out=None, out_dtype=torc
 
 def linear_mxfp4_forward(x, w: MxOperand, bias=None, ws=None, stream=None, check=True):
     """``x`` [m, k] (quantised here) times the transpose of the weight operand
-    ``w`` [n, k] (``quantize_mxfp4`` of the weight), in the dtype of ``x``."""
+    ``w`` [n, k] (``quantize_mxfp4`` of the weight), in the dtype of ``x``;
+    ``ws`` and ``check`` as in :func:`matmul_mxfp4`."""
+    _readable(ws, check)
     m, k = _matrix(x)
     index = x.get_device()
     w_codes, w_scales, n, kw = _operand(w, "w", index)
@@ -756,7 +767,9 @@ def linear_mxfp4_backward(dy, x, w_t: MxOperand, dw=None, ws=None, stream=None, 
     ``dy`` and ``dw`` [n, k] fp32 (added to ``dw`` where it is given), each a
     product of operands quantised along its own contraction (the quantiser is
     passed straight through).  ``w_t``: ``quantize_mxfp4(weight,
-    along_rows=True)``.  The bias's gradient is ``dy.sum(0)``."""
+    along_rows=True)``.  The bias's gradient is ``dy.sum(0)``.  ``ws`` and
+    ``check`` as in :func:`matmul_mxfp4`."""
+    _readable(ws, check)
     m, n = _matrix(dy, "dy")
     mx, k = _matrix(x)
     index = dy.get_device()

@@ -372,18 +372,22 @@ def jfa_quantize_mxfp4_both(x, dtype, rows, cols, codes, scales, codes_t, scales
                                           _addr(scales_t), _stream(stream)))
 
 
+def _nbytes(t, given=None) -> int:
+    """The bytes behind a buffer's address.  A strided or expanded tensor does
+    not have the memory that its element count says."""
+    if given is not None:
+        return int(given)
+    if not isinstance(t, torch.Tensor) or not t.is_contiguous():
+        _invalid("a workspace or scratch buffer must be a contiguous tensor, or its size be given")
+    return t.numel() * t.element_size()
+
+
 def jfa_matmul_mxfp4(m, n, k, a_codes, a_scales, b_codes, b_scales, bias, out, out_dtype,
                      accumulate, workspace, ws_bytes=None, stream=None):
-    if ws_bytes is None:
-        ws_bytes = workspace.numel() * workspace.element_size()
     _check(load().jfa_matmul_mxfp4(int(m), int(n), int(k), _addr(a_codes), _addr(a_scales),
                                    _addr(b_codes), _addr(b_scales), _addr(bias), _addr(out),
                                    DTYPE.get(out_dtype, out_dtype), int(bool(accumulate)),
-                                   _addr(workspace), int(ws_bytes), _stream(stream)))
-
-
-def _nbytes(t, given=None) -> int:
-    return int(given) if given is not None else t.numel() * t.element_size()
+                                   _addr(workspace), _nbytes(workspace, ws_bytes), _stream(stream)))
 
 
 def jfa_linear_mxfp4_scratch_bytes(m, n, k, backward) -> int:
@@ -431,15 +435,13 @@ def jfa_block_norm_forward(desc, x, block, gate, scale, post_gamma, post_beta, p
 def jfa_block_norm_backward(desc, x, block, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta,
                             dy, dn, dx, dblock, dgate, dscale, dpost_gamma, dpost_beta, dpre_gamma,
                             dpre_beta, workspace, ws_bytes=None, stream=None):
-    if ws_bytes is None:
-        ws_bytes = workspace.numel() * workspace.element_size()
     _check(load().jfa_block_norm_backward(ctypes.byref(desc), _addr(x), _addr(block), _addr(gate),
                                           _addr(scale), _addr(post_gamma), _addr(post_beta),
                                           _addr(pre_gamma), _addr(pre_beta), _addr(dy), _addr(dn),
                                           _addr(dx), _addr(dblock), _addr(dgate), _addr(dscale),
                                           _addr(dpost_gamma), _addr(dpost_beta), _addr(dpre_gamma),
-                                          _addr(dpre_beta), _addr(workspace), int(ws_bytes),
-                                          _stream(stream)))
+                                          _addr(dpre_beta), _addr(workspace),
+                                          _nbytes(workspace, ws_bytes), _stream(stream)))
 
 
 def jfa_test_inject(what: int):
@@ -689,6 +691,13 @@ def _ws_on(ws, index):
     """The caller's workspace, on the GPU, or a fresh one."""
     if ws is None:
         return mxfp4_workspace(torch.device("cuda", index))
+    return _buffer(ws, index)
+
+
+def _buffer(ws, index):
+    """A workspace of the caller's: memory of that GPU, all of it behind its address."""
+    if not isinstance(ws, torch.Tensor) or not ws.is_contiguous():
+        _invalid("ws: a contiguous torch tensor is needed")
     if ws.get_device() != index:
         _invalid(f"ws: device {ws.device}, expected cuda:{index}")
     return ws
@@ -870,8 +879,8 @@ def block_norm_backward(desc: jfa_block_norm, x, block, gate=None, scale=None, p
             return block_norm_backward(desc, x, block, gate, *params, dy=dy, dn=dn, ws=ws)
     if ws is None:
         ws = block_norm_workspace(desc, x.device)
-    elif ws.get_device() != index:
-        _invalid(f"ws: device {ws.device}, expected cuda:{index}")
+    else:
+        _buffer(ws, index)
     dx, dblock, dgate = torch.empty_like(x), torch.empty_like(x), _like(gate)
     dscale, dpost_gamma, dpost_beta = _like(scale), _like(post_gamma), _like(post_beta)
     dpre_gamma, dpre_beta = _like(pre_gamma), _like(pre_beta)

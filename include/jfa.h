@@ -318,16 +318,23 @@ jfa_status jfa_quantize_mxfp4_both(const void* x, jfa_dtype dtype, int64_t rows,
  * weight [n][k] as a linear layer keeps it); bias: device fp32 [n] or NULL;
  * out: device [m][n], out_dtype JFA_F32 or JFA_BF16, 16-byte aligned, must not
  * overlap the operands; accumulate != 0 adds to what out holds (gradient
- * accumulation; an fp32 sum below 2^-126 may come out as zero).  The gradients of a linear layer y = x w^T are products of
- * the same kind: dx = dy w (operands dy along rows, w with along_rows = 1),
- * dw = dy^T x (both with along_rows = 1).  The order of the sums depends only
- * on the sizes: equal calls give equal bits.
+ * accumulation; an fp32 sum below 2^-126 may come out as zero).  The gradients
+ * of a linear layer y = x w^T are products of the same kind: dx = dy w
+ * (operands dy along rows, w with along_rows = 1), dw = dy^T x (both with
+ * along_rows = 1).  The order of the sums depends only on the sizes: equal
+ * calls give equal bits.
  * m, n, k in [0, 2^30]; m or n = 0 is a no-op, k = 0 an empty sum.
  * workspace: jfa_mxfp4_workspace_bytes() bytes, 16-byte aligned, ZEROED by the
  * caller once before its first use: it holds only the device error word,
- * which stays set (JFA_ERR_TIMEOUT, results undefined) until jfa_check_error
- * reads and clears it, so calls on several streams and captured graphs may
- * share one.  Nothing is kept in it between calls. */
+ * which stays set (JFA_ERR_TIMEOUT) until jfa_check_error reads and clears it.
+ * A call whose waits find it set may give up too, without a mark of its own, so
+ * the word speaks for all calls that used the workspace since it was last
+ * read: the results of all of them are undefined then.  Calls and captured
+ * graphs of one stream may share one.  Calls of several streams may share one
+ * only if it is read once, after all of them have completed; where a stream is
+ * to be checked by itself it needs its own (a read that clears the word while
+ * another stream's call is under way would hide that call's failure).  Nothing
+ * else is kept in it between calls. */
 size_t jfa_mxfp4_workspace_bytes(void);
 jfa_status jfa_matmul_mxfp4(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
                             const uint8_t* a_scales, const uint8_t* b_codes,

@@ -603,7 +603,10 @@ def _switch(device, stream):
 
 
 def mxfp4_workspace(device) -> torch.Tensor:
-    """The zeroed workspace of :func:`matmul_mxfp4` (an error word; may be shared)."""
+    """The zeroed workspace of :func:`matmul_mxfp4` and the linear layer: an
+    error word, for one stream's calls.  Calls of several streams may share one
+    only with ``check=False`` and one ``jfa_check_error(ws)`` after all of them
+    have completed; what that raises concerns them all."""
     return torch.zeros(jfa_mxfp4_workspace_bytes(), dtype=_U8, device=device)
 
 

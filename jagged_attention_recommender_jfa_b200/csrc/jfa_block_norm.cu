@@ -234,7 +234,7 @@ struct Cols {
 // limits the warps of an SM with up to eight elements per thread and tensor, and
 // those hide the latencies of the row sums; and what spills in wide rows (us in
 // registers / in shared memory: 10000 x 8192 fp32 RMS forward 356 / 320,
-// backward 733 / 671, 15000 x 6000 bf16 LayerNorm 402 / 355 and 769 / 802).
+// backward 733 / 671, 15000 x 6000 bf16 LayerNorm forward 402 / 355).
 template <int K, int P, bool MEM>
 struct Params {
     float2 v[K][P];
@@ -476,8 +476,13 @@ template <typename T, int NCH, bool LN>
 constexpr bool kSumsInSmem = NCH * Vec<T>::N > 8 || LN;
 template <bool LN>
 constexpr int kBwdParams = LN ? 3 : 2;
+// Except beside the four sums of bf16 LayerNorms with two vectors per thread,
+// where the 168 registers of up to 384 threads hold the parameters (us in
+// registers / in shared memory: 15000 x 6000 769 / 804, 6144 746 / 795, 4200
+// 695 / 699, 5003 805 / 806; with 512 threads they fit in registers only).
 template <typename T, int NCH, bool LN, int BOUND>
-constexpr bool kBwdParamsInSmem = kFits<T, NCH, kBwdParams<LN> + (kSumsInSmem<T, NCH, LN> ? (LN ? 4 : 2) : 0), BOUND>;
+constexpr bool kBwdParamsInSmem = !(LN && sizeof(T) == 2 && NCH == 2) &&
+                                  kFits<T, NCH, kBwdParams<LN> + (kSumsInSmem<T, NCH, LN> ? (LN ? 4 : 2) : 0), BOUND>;
 template <int P, int Q, bool SMEM>
 struct Sums {
     float2 v[Q][P];

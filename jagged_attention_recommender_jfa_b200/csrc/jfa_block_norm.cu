@@ -405,11 +405,15 @@ constexpr int kFwdBound = NCH > 1 ? (sizeof(T) == 4 && NCH == 2 ? 640 : kMaxThre
 template <typename T, int NCH>
 constexpr int kBwdBound = NCH == 1 && sizeof(T) == 4 ? 768 : kMaxThreads;
 
-// bf16 rows of two vectors per thread spill at 128 registers; up to 384 threads
-// (6144 columns) there are 168.
+// bf16 rows of two and three vectors per thread spill at 128 registers; up to
+// 384 threads there are 168.  Two vectors need no more up to 6144 columns, three
+// never do (352; 10000 x 8191, us at 512 / 384: RMS forward 308 / 250, backward
+// 817 / 587, LayerNorm 517 / 408 and 1110 / 821).  fp32 rows of five vectors have 416 threads, for which there
+// are 128 again: the registers are dealt to the SM's four schedulers, and 13
+// warps are four on one of them.
 constexpr int kFewThreads = 384;
 template <typename T, int BOUND>
-constexpr int kTwoBound = sizeof(T) == 2 ? kFewThreads : BOUND;
+constexpr int kFewBound = sizeof(T) == 2 ? kFewThreads : BOUND;
 
 // LN: a norm is a LayerNorm, so that there may be betas.
 template <typename T, int NCH, bool LN, int BOUND = kFwdBound<T, NCH>>
@@ -844,10 +848,10 @@ Kernel fwd_kernel_of(const RowShape& s) {
     constexpr int M = kMostChunks<T>;
     switch (s.nch) {
         case 1: return fwd_kernel<T, 1, LN>();
-        case 2: return s.threads <= kFewThreads ? fwd_kernel<T, 2, LN, kTwoBound<T, kFwdBound<T, 2>>>() : fwd_kernel<T, 2, LN>();
-        case 3: return fwd_kernel<T, 3, LN>();
-        case 4: return fwd_kernel<T, M < 4 ? M : 4, LN>();
-        default: return fwd_kernel<T, M, LN>();
+        case 2: return s.threads <= kFewThreads ? fwd_kernel<T, 2, LN, kFewBound<T, kFwdBound<T, 2>>>() : fwd_kernel<T, 2, LN>();
+        case 3: return fwd_kernel<T, 3, LN, kFewBound<T, kFwdBound<T, 3>>>();
+        case 4: return fwd_kernel<T, M < 4 ? M : 4, LN, kFewBound<T, kFwdBound<T, 4>>>();
+        default: return fwd_kernel<T, M, LN, kFewBound<T, kFwdBound<T, M>>>();
     }
 }
 template <typename T, bool LN>
@@ -855,10 +859,10 @@ Kernel bwd_kernel_of(const RowShape& s) {
     constexpr int M = kMostChunks<T>;
     switch (s.nch) {
         case 1: return bwd_kernel<T, 1, LN>();
-        case 2: return s.threads <= kFewThreads ? bwd_kernel<T, 2, LN, kTwoBound<T, kBwdBound<T, 2>>>() : bwd_kernel<T, 2, LN>();
-        case 3: return bwd_kernel<T, 3, LN>();
-        case 4: return bwd_kernel<T, M < 4 ? M : 4, LN>();
-        default: return bwd_kernel<T, M, LN>();
+        case 2: return s.threads <= kFewThreads ? bwd_kernel<T, 2, LN, kFewBound<T, kBwdBound<T, 2>>>() : bwd_kernel<T, 2, LN>();
+        case 3: return bwd_kernel<T, 3, LN, kFewBound<T, kBwdBound<T, 3>>>();
+        case 4: return bwd_kernel<T, M < 4 ? M : 4, LN, kFewBound<T, kBwdBound<T, 4>>>();
+        default: return bwd_kernel<T, M, LN, kFewBound<T, kBwdBound<T, M>>>();
     }
 }
 

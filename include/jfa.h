@@ -560,11 +560,11 @@ jfa_status jfa_forward_fixed_scratch(const jfa_problem* problem, const void* q, 
  * the tensor-core kernel: CTA 0 skips its first key-tile load and the waits
  * give up after 5 ms instead of 1 s, so the call ends with JFA_ERR_TIMEOUT in
  * the workspace's error word (jfa_check_error) while every copy the kernel
- * did issue completes.  JFA_TEST_MATMUL_SKIP_LOAD does the same to the thread's
- * next jfa_matmul_mxfp4 that computes a product (m, n, k > 0), whose result is
- * then undefined.  what = 0 disarms.  The hook is used up by that call (or by
- * any jfa_forward on the CUDA-core path).  JFA_ERR_INVALID_ARGUMENT for another
- * value. */
+ * did issue completes.  That call uses the hook up, and so does any jfa_forward
+ * on the CUDA-core path.  JFA_TEST_MATMUL_SKIP_LOAD does the same to the
+ * thread's next jfa_matmul_mxfp4 that computes a product (m, n, k > 0), whose
+ * result is then undefined, whatever other calls come before it.  what = 0
+ * disarms.  JFA_ERR_INVALID_ARGUMENT for another value. */
 enum { JFA_TEST_FWD_SKIP_LOAD = 1, JFA_TEST_MATMUL_SKIP_LOAD = 2 };
 jfa_status jfa_test_inject(int what);
 

@@ -61,7 +61,7 @@ struct Profiler {
 };
 thread_local Profiler g_prof;
 thread_local char g_msg[512] = "";
-thread_local int g_test_hook = 0;       // jfa_test_inject: armed for the next forward
+thread_local int g_test_hook = 0;       // jfa_test_inject: armed for the next call of its kind
 
 const char* const kKernelNames[K_COUNT] = {
     "sched_prepare", "sched_rank", "simt_fwd", "simt_bwd_pre", "simt_bwd_dq", "simt_bwd_dkdv",
@@ -215,8 +215,7 @@ jfa_status forward_impl(const jfa_problem* problem, const void* q, const void* k
     WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
     const bool tc = use_tc(p, act, 0);
     const int tile = tc ? tc_fwd_tile() : kSimtFwdTile;
-    const bool inject = tc && g_test_hook == JFA_TEST_FWD_SKIP_LOAD;
-    g_test_hook = 0;
+    const bool armed = take_test_hook(JFA_TEST_FWD_SKIP_LOAD) != 0, inject = tc && armed;
     cudaError_t e = build_schedule(p, q_offsets, kv_offsets, causal, 0, tile, hdr,
                                    reinterpret_cast<int64_t*>(ws + L.dense_off),
                                    reinterpret_cast<int2*>(ws + L.pair_bt),

@@ -58,3 +58,22 @@ def test_streams_that_share_a_workspace_are_checked_together(cuda_device, produc
         torch.cuda.synchronize()
         jfa.jfa_check_error(ws)
         assert all(torch.equal(g, p[2]) for g, p in zip(got, products))
+
+
+def test_an_attention_call_leaves_a_product_armed(cuda_device, products):
+    # the injected failure reaches the product that it is meant for
+    q = torch.randn(64, 1, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(cuda_device)
+    off = torch.tensor([0, 64], dtype=torch.int32, device=cuda_device)
+    prob = jfa.make_problem(batch=1, heads=1, head_dim=128, max_q_len=64, max_kv_len=64, total_q=64, total_kv=64,
+                            dtype="bf16")
+    assert jfa.jfa_path(prob, "softmax", 0) == 1
+    want = jfa.attention_forward(prob, q, q, q, off, off)[0]
+    ws = jfa.mxfp4_workspace(cuda_device)
+    torch.cuda.synchronize()
+    jfa.jfa_test_inject(jfa.JFA_TEST_MATMUL_SKIP_LOAD)
+    assert torch.equal(jfa.attention_forward(prob, q, q, q, off, off)[0], want)
+    run(products[0], ws)
+    timed_out(ws, products[0][3])
+    got = run(products[0], ws)
+    jfa.jfa_check_error(ws, products[0][3])
+    assert torch.equal(got, products[0][2])

@@ -25,8 +25,10 @@
 // Bound: HBM.  Forward 3 tensors read and 2 written, backward 5 read and 3
 // written.  Persistent groups of threads take rows in turn, a row's values in
 // registers, one 16-byte vector per thread, tensor and chunk; the next row's
-// vectors are loaded before the current row is worked on, and the parameters
-// stay in registers.  Statistics are taken from the registers: centred sums, so
+// vectors are loaded before the current row is worked on (in the backward where
+// a thread has one vector per tensor: more leave no registers for it), and the
+// parameters wait in shared memory where they fit (Params, kBwdParamsInSmem).
+// Statistics are taken from the registers: centred sums, so
 // that a large mean costs no digits.  Parameter gradients are summed per thread
 // over the group's rows, written as one partial row per CTA and summed in a
 // fixed order by a second small kernel: no atomics, the same result every time.

@@ -1,10 +1,9 @@
 // MXFP4 (OCP Microscaling v1.0: E2M1 elements, one E8M0 scale per 32) helpers
-// shared by the quantisers, the norms and the product: shared exponents, the
-// hardware E2M1 conversions and the layout of the scales.
+// shared by the quantisers and the product: shared exponents, the hardware E2M1
+// conversions and the layout of the scales.
 #pragma once
 
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 #include <stdint.h>
 
 #include "jfa_sm100.cuh"

@@ -410,9 +410,9 @@ constexpr int kBwdBound = NCH == 1 && sizeof(T) == 4 ? 768 : kMaxThreads;
 // bf16 rows of two and three vectors per thread spill at 128 registers; up to
 // 384 threads there are 168.  Two vectors need no more up to 6144 columns, three
 // never do (352; 10000 x 8191, us at 512 / 384: RMS forward 308 / 250, backward
-// 817 / 587, LayerNorm 517 / 408 and 1110 / 821).  fp32 rows of five vectors have 416 threads, for which there
-// are 128 again: the registers are dealt to the SM's four schedulers, and 13
-// warps are four on one of them.
+// 817 / 587, LayerNorm 517 / 408 and 1110 / 821).  fp32 rows of five vectors
+// have 416 threads, for which there are 128 again: the registers are dealt to
+// the SM's four schedulers, and 13 warps are four on one of them.
 constexpr int kFewThreads = 384;
 template <typename T, int BOUND>
 constexpr int kFewBound = sizeof(T) == 2 ? kFewThreads : BOUND;
@@ -485,7 +485,7 @@ constexpr int kBwdParams = LN ? 3 : 2;
 // Except beside the four sums of bf16 LayerNorms with two vectors per thread,
 // where the 168 registers of up to 384 threads hold the parameters (us in
 // registers / in shared memory: 15000 x 6000 769 / 804, 6144 746 / 795, 4200
-// 695 / 699, 5003 805 / 806; with 512 threads they fit in registers only).
+// 695 / 699, 5003 805 / 806; beside the sums of 512 threads they do not fit).
 template <typename T, int NCH, bool LN, int BOUND>
 constexpr bool kBwdParamsInSmem = !(LN && sizeof(T) == 2 && NCH == 2) &&
                                   kFits<T, NCH, kBwdParams<LN> + (kSumsInSmem<T, NCH, LN> ? (LN ? 4 : 2) : 0), BOUND>;
